@@ -408,6 +408,104 @@ pwq_status nvfp4_quant_grouped_mma(int n_groups, const int* group_sizes, const p
                                    void* workspace, size_t workspace_bytes, pwq_stream_t stream);
 
 /* ===================================================================== */
+/* Block-scaled products                                                  */
+/* ===================================================================== */
+/*
+ * The product that a quantised linear layer's rollout runs on ("Low Precision
+ * RL", "Modes" 3 and 4; verl NVFP4 QAT article 2.5): activations a [B][M][K]
+ * times weights w [B][N][K], both quantised along K, into BF16 y [B][M][N]:
+ *
+ *   y[b][m][n] = bf16(ga_b gw_b sum_k dec(a[b][m][k]) sa[b][m][k / V]
+ *                                    dec(w[b][n][k]) sw[b][n][k / V])
+ *
+ * MXFP8: V = 32, E4M3 codes, UE8M0 scales, ga = gw = 1.  NVFP4: V = 16,
+ * packed E2M1 codes, E4M3 block scales (non-negative, as the quantisers
+ * write them), FP32 global scales [B] of each operand.  The products of
+ * codes and scales are exact and accumulated by the tensor core in FP32 (the
+ * order of the sum is the hardware's; calls with the same arguments give
+ * the same bits); the FP32 sum times ga_b gw_b is rounded to BF16 once.
+ * NaN scale bytes (0xff UE8M0, 0x7f E4M3) and NaN codes give NaN in the
+ * rows and columns that they meet.
+ *
+ * Scales are in the tile layout above with zero padding, as
+ * pwq_scales_to_mma, mxfp8_quant_grouped_mma, nvfp4_quant_grouped_mma and
+ * the norms below write it: pwq_mma_scale_bytes(B, rows, K / V) bytes,
+ * 16-byte aligned.
+ *
+ * K % V == 0; any M, N >= 1.  Code tensors: base, row and batch strides
+ * multiples of 16 bytes (an NVFP4 K that is no multiple of 32 needs padded
+ * rows).  y: 2-byte aligned, any row stride >= N (16-byte aligned rows
+ * are written with wider stores).  K = 0 writes zeros.  y may not overlap an
+ * operand.  Errors: PWQ_ERR_NULL, _ALIGN, _SHAPE (also more than 2^27
+ * output tiles), _STRIDE, _OVERLAP, _CUDA.  A device wait that gives up (2 s)
+ * sets bit 2 of pwq_device_error(). */
+pwq_status mxfp8_matmul(const pwq_tensor* a, const uint8_t* a_scale_mma, const pwq_tensor* w,
+                        const uint8_t* w_scale_mma, const pwq_tensor* y, pwq_stream_t stream);
+pwq_status nvfp4_matmul(const pwq_tensor* a_packed, const uint8_t* a_sb_mma, const float* a_global_scale,
+                        const pwq_tensor* w_packed, const uint8_t* w_sb_mma, const float* w_global_scale,
+                        const pwq_tensor* y, pwq_stream_t stream);
+
+/* ===================================================================== */
+/* Residual RMS norm with a block-scaled output                           */
+/* ===================================================================== */
+/*
+ * The step in front of every quantised linear layer (rollout, and the
+ * forward of quantisation-aware training; "Low Precision RL", "Modes" 3 and
+ * 4, verl NVFP4 QAT article 2.2, 2.3), in one launch:
+ *
+ *   h = bf16(fl(x + residual))              (h = x when residual is NULL)
+ *   rstd_m = (sum_d h[m][d]^2 / D + eps)^(-1/2)
+ *   y[m][d] = bf16(h[m][d] rstd_m weight[d])
+ *
+ * and the output is that of mxfp8_quant(y), or of nvfp4_quant(y, amax_in),
+ * bit for bit (the *_fake_quant forms: their dequantised BF16 values).  y
+ * is the BF16 nearest to the product of h, weight and the 64-bit rstd of the
+ * exact sum of squares, so the codes do not depend on an order of addition.
+ *
+ * x         BF16 [B][M][D], D % 32 == 0 (MXFP8) / % 16 == 0 (NVFP4), D <= 32768.
+ * residual  BF16 like x, or NULL.  weight: BF16 [D], 16-byte aligned.
+ * eps       in [1e-16, 1e30] (else PWQ_ERR_ARG).
+ * amax_in   NVFP4: FP32 [B], the activation's amax (an observer's); values
+ *           beyond it saturate.
+ * h         BF16 output, given exactly when residual is (else
+ *           PWQ_ERR_ARG); may be x or residual exactly (in place).
+ * q, scale  codes and block scales as mxfp8_quant / nvfp4_quant write them;
+ *           scale_mma / sb_mma = 1: the tile layout instead of the dense one
+ *           (4-byte aligned, pwq_mma_scale_bytes() bytes, padding written as zero).
+ * global_scale  NVFP4 codes: FP32 [B], fl(amax_in / 2688).
+ * rstd      optional FP32 [B][M] output (for rms_norm_backward).
+ * Errors: PWQ_ERR_NULL, _ALIGN, _SHAPE, _STRIDE, _OVERLAP, _ARG, _CUDA. */
+pwq_status rms_norm_mxfp8(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                          const pwq_tensor* h, const pwq_tensor* q, uint8_t* scale, int scale_mma, float* rstd,
+                          pwq_stream_t stream);
+pwq_status rms_norm_nvfp4(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                          const float* amax_in, const pwq_tensor* h, const pwq_tensor* q_packed, uint8_t* sb,
+                          int sb_mma, float* global_scale, float* rstd, pwq_stream_t stream);
+pwq_status rms_norm_mxfp8_fake_quant(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                                     const pwq_tensor* h, const pwq_tensor* y, float* rstd, pwq_stream_t stream);
+pwq_status rms_norm_nvfp4_fake_quant(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                                     const float* amax_in, const pwq_tensor* h, const pwq_tensor* y, float* rstd,
+                                     pwq_stream_t stream);
+
+/* rms_norm_backward: the gradient of the norm, the quantiser straight
+ * through (verl NVFP4 QAT article 2.3).  With xhat = h rstd, g = dy weight
+ * and c_m = sum_d g xhat / D, in FP32:
+ *   dx = bf16(rstd (g - c xhat) + dh)   (the gradient of x and of residual)
+ *   dweight[d] = sum_m dy xhat          (summed in a fixed order)
+ * dy, h     BF16 [B][M][D] (D % 16 == 0, D <= 32768); rstd FP32 [B][M].
+ * dh        BF16 gradient of the output h, or NULL (zero).
+ * dx        BF16 output.  dweight: FP32 [D] (dweight_bf16 = 0) or BF16 [D]
+ *           (1) output, or NULL (then workspace may be NULL).
+ * workspace 16-byte aligned, rms_norm_backward_workspace_size(h) bytes on
+ *           the device that is current; contents on entry do not matter.
+ * An empty h writes dweight = 0.  Errors: PWQ_ERR_NULL, _ALIGN, _SHAPE,
+ * _STRIDE, _OVERLAP, _WORKSPACE, _ARG, _CUDA. */
+size_t rms_norm_backward_workspace_size(const pwq_tensor* h);
+pwq_status rms_norm_backward(const pwq_tensor* dy, const pwq_tensor* dh, const pwq_tensor* h, const void* weight,
+                             const float* rstd, const pwq_tensor* dx, void* dweight, int dweight_bf16,
+                             void* workspace, size_t workspace_bytes, pwq_stream_t stream);
+
+/* ===================================================================== */
 /* FP8 block-wise weights into a rollout format                           */
 /* ===================================================================== */
 
@@ -536,7 +634,8 @@ const char* pwq_build_info(void);
 
 /* Reads and clears the device-side error word of the current device
  * (synchronous; 0 = no error; bit 0 = a TMA load wait gave up, bit 1 = an
- * NVFP4 single-pass encode item gave up waiting for its group amax).  When
+ * NVFP4 single-pass encode item gave up waiting for its group amax, bit 2 =
+ * a wait inside a block-scaled product gave up).  When
  * a bit is set, the outputs of the calls since the previous read are
  * unspecified.  Returns PWQ_ERR_NULL or PWQ_ERR_CUDA on failure. */
 pwq_status pwq_device_error(uint32_t* code);

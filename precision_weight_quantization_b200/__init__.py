@@ -12,6 +12,7 @@ Functions take CUDA tensors ([M, N] or batched [B, M, N], last dimension
 contiguous) and return newly allocated outputs unless ``out=`` buffers are
 given.  Nothing synchronises.
 """
+import contextlib
 import ctypes
 from typing import List, Optional, Sequence, Tuple
 
@@ -29,7 +30,8 @@ __all__ = [
     "nvfp4_fake_quant_grouped", "fp8_block_requant", "fp8_block_requant_mxfp8", "fp8_block_requant_nvfp4",
     "fp8_block_requant_nvfp4_grouped", "fp8_block_requant_grouped", "fp8_block_requant_mxfp8_grouped",
     "NVFP4ActivationObserver", "nvfp4_w4a4_fake_quant_ste", "OBSERVERS", "mma_scale_bytes", "scales_to_mma",
-    "scales_from_mma", "mxfp8_quant_grouped_mma", "nvfp4_quant_grouped_mma",
+    "scales_from_mma", "mxfp8_quant_grouped_mma", "nvfp4_quant_grouped_mma", "mxfp8_matmul", "nvfp4_matmul",
+    "rms_norm_mxfp8", "rms_norm_nvfp4", "rms_norm_fake_quant", "rms_norm_backward", "rms_norm_fake_quant_ste",
 ]
 
 _CODE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
@@ -571,6 +573,275 @@ def nvfp4_quant_grouped_mma(groups: Sequence[Sequence[torch.Tensor]], out=None, 
                                       _ptrs([s for g in sb for s in g]), _ptrs(global_scale), ws.data_ptr(),
                                       ws.numel(), _stream(flat[0])), "nvfp4_quant_grouped_mma")
     return out, sb, global_scale
+
+
+# ---------------------------------------------------------------- block-scaled products
+
+def _same_device(ts):
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on different devices: %s and %s" % (dev, t.device))
+
+
+def _on_device(t: torch.Tensor):
+    """Makes t's device current for a call (the library launches on the current device)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+
+
+def _mma_scales(scale: torch.Tensor, B: int, rows: int, cols: int, name: str) -> torch.Tensor:
+    n = B * -(-rows // 128) * -(-cols // 4) * 512
+    if scale.element_size() != 1 or not scale.is_contiguous() or scale.numel() != n:
+        raise ValueError("%s must be a contiguous one-byte tensor of the %d bytes of the tile layout (scales_to_mma)"
+                         % (name, n))
+    return scale
+
+
+def _product(a, w, out, fp4):
+    per = 2 if fp4 else 1
+    if a.dim() != w.dim():
+        raise ValueError("a and w must both be 2-D or both 3-D, got %s and %s" % (tuple(a.shape), tuple(w.shape)))
+    B, M, K = _batch(a), a.shape[-2], a.shape[-1] * per
+    N = w.shape[-2]
+    if out is None:
+        out = torch.empty(a.shape[:-1] + (N,), dtype=torch.bfloat16, device=a.device)
+    _check_dtype(out, (torch.bfloat16,), "out")
+    return B, M, N, K, out
+
+
+def mxfp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """BF16 y = a w^T of MXFP8 operands: codes a [.., M, K] and w [.., N, K]
+    (2-D or batched alike), UE8M0 scales in the tensor-core tile layout
+    (mxfp8_quant_grouped_mma, scales_to_mma, rms_norm_mxfp8).  Block scales
+    and products are exact, the sum is FP32, y is rounded once.  Code rows
+    are 16-byte aligned; ``out`` may have any row stride.  No gradient: codes
+    are not differentiable."""
+    _check_dtype(a, _CODE_DTYPES, "a")
+    _check_dtype(w, _CODE_DTYPES, "w")
+    B, M, N, K, out = _product(a, w, out, False)
+    _same_device((a, a_scale, w, w_scale, out))
+    da, dw, dy = _desc(a, "a"), _desc(w, "w"), _desc(out, "out")
+    sa, sw = _mma_scales(a_scale, B, M, K // 32, "a_scale"), _mma_scales(w_scale, B, N, K // 32, "w_scale")
+    with _on_device(a):
+        check(lib.mxfp8_matmul(ctypes.byref(da), sa.data_ptr(), ctypes.byref(dw), sw.data_ptr(), ctypes.byref(dy),
+                               _stream(a)), "mxfp8_matmul")
+    return out
+
+
+def nvfp4_matmul(a: torch.Tensor, a_sb: torch.Tensor, a_global_scale: torch.Tensor, w: torch.Tensor,
+                 w_sb: torch.Tensor, w_global_scale: torch.Tensor,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """BF16 y = a w^T of NVFP4 operands (W4A4): packed codes a [.., M, K/2]
+    and w [.., N, K/2], E4M3 block scales in the tensor-core tile layout
+    (nvfp4_quant_grouped_mma, scales_to_mma, rms_norm_nvfp4), FP32 global
+    scales [B].  As mxfp8_matmul otherwise."""
+    _check_dtype(a, (torch.uint8,), "a")
+    _check_dtype(w, (torch.uint8,), "w")
+    B, M, N, K, out = _product(a, w, out, True)
+    _same_device((a, a_sb, a_global_scale, w, w_sb, w_global_scale, out))
+    da, dw, dy = _desc(a, "a", True), _desc(w, "w", True), _desc(out, "out")
+    sa, sw = _mma_scales(a_sb, B, M, K // 16, "a_sb"), _mma_scales(w_sb, B, N, K // 16, "w_sb")
+    for g, name in ((a_global_scale, "a_global_scale"), (w_global_scale, "w_global_scale")):
+        if g.dtype != torch.float32 or not g.is_contiguous() or g.numel() != B:
+            raise ValueError("%s must be a contiguous float32 tensor of %d values" % (name, B))
+    with _on_device(a):
+        check(lib.nvfp4_matmul(ctypes.byref(da), sa.data_ptr(), a_global_scale.data_ptr(), ctypes.byref(dw),
+                               sw.data_ptr(), w_global_scale.data_ptr(), ctypes.byref(dy), _stream(a)),
+              "nvfp4_matmul")
+    return out
+
+
+# ---------------------------------------------------------------- residual RMS norm with a block-scaled output
+
+def _norm_inputs(x, weight, residual, amax):
+    """Checks shared by the norms; returns (descriptor refs of x and residual, B)."""
+    _check_dtype(x, (torch.bfloat16,), "x")
+    _check_dtype(weight, (torch.bfloat16,), "weight")
+    B = _batch(x)
+    if weight.dim() != 1 or weight.shape[0] != x.shape[-1] or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous 1-D tensor of %d values" % x.shape[-1])
+    if residual is not None:
+        _check_dtype(residual, (torch.bfloat16,), "residual")
+    if amax is not None and (amax.dtype != torch.float32 or not amax.is_contiguous() or amax.numel() != B):
+        raise ValueError("amax must be a contiguous float32 tensor of %d values" % B)
+    _same_device((x, weight, residual, amax))
+    dr = ctypes.byref(_desc(residual, "residual")) if residual is not None else None
+    return _desc(x, "x"), dr, B
+
+
+def _norm_h(x, residual, h):
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is an output of the residual form only")
+        return x, None
+    h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if h is None else h
+    _check_dtype(h, (torch.bfloat16,), "h")
+    return h, ctypes.byref(_desc(h, "h"))
+
+
+def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                   eps: float = 1e-6, mma: bool = True, out: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None):
+    """h = x + residual; y = h * rsqrt(mean(h^2) + eps) * weight; MXFP8 of y,
+    in one launch (include/pwq.h).  x [.., M, D] BF16, weight [D] BF16.
+    Returns (codes float8_e4m3fn [.., M, D], UE8M0 scales, h): scales in the
+    tensor-core tile layout (mma=True, for mxfp8_matmul) or dense
+    [.., M, D/32]; h is x itself without a residual, and ``h=residual``
+    updates the residual in place."""
+    dx, dr, B = _norm_inputs(x, weight, residual, None)
+    M, D = x.shape[-2:]
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    _check_dtype(out, _CODE_DTYPES, "out")
+    if scale is None:
+        shape = (mma_scale_bytes(B, M, D // 32),) if mma else x.shape[:-1] + (D // 32,)
+        scale = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    if mma:
+        _mma_scales(scale, B, M, D // 32, "scale")
+    elif scale.element_size() != 1 or not scale.is_contiguous() or scale.numel() != B * M * (D // 32):
+        raise ValueError("scale must be a contiguous one-byte tensor [.., M, D/32]")
+    hh, dh = _norm_h(x, residual, h)
+    _same_device((x, out, scale, hh))
+    dq = _desc(out, "out")
+    with _on_device(x):
+        check(lib.rms_norm_mxfp8(ctypes.byref(dx), dr, weight.data_ptr(), eps, dh, ctypes.byref(dq),
+                                 scale.data_ptr(), int(mma), None, _stream(x)), "rms_norm_mxfp8")
+    return out, scale, hh
+
+
+def rms_norm_nvfp4(x: torch.Tensor, weight: torch.Tensor, amax: torch.Tensor,
+                   residual: Optional[torch.Tensor] = None, eps: float = 1e-6, mma: bool = True,
+                   out: Optional[torch.Tensor] = None, sb: Optional[torch.Tensor] = None,
+                   global_scale: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None):
+    """rms_norm_mxfp8 with NVFP4 output for a given activation amax (float32
+    [B], an NVFP4ActivationObserver's).  Returns (packed codes uint8
+    [.., M, D/2], block scales, global scales float32 [B], h)."""
+    dx, dr, B = _norm_inputs(x, weight, residual, amax)
+    M, D = x.shape[-2:]
+    if out is None:
+        out = torch.empty(x.shape[:-1] + (D // 2,), dtype=torch.uint8, device=x.device)
+    _check_dtype(out, (torch.uint8,), "out")
+    if sb is None:
+        sb = (torch.empty(mma_scale_bytes(B, M, D // 16), dtype=torch.uint8, device=x.device) if mma else
+              torch.empty(x.shape[:-1] + (D // 16,), dtype=torch.float8_e4m3fn, device=x.device))
+    if mma:
+        _mma_scales(sb, B, M, D // 16, "sb")
+    elif sb.element_size() != 1 or not sb.is_contiguous() or sb.numel() != B * M * (D // 16):
+        raise ValueError("sb must be a contiguous one-byte tensor [.., M, D/16]")
+    if global_scale is None:
+        global_scale = torch.empty(B, dtype=torch.float32, device=x.device)
+    if global_scale.dtype != torch.float32 or not global_scale.is_contiguous() or global_scale.numel() != B:
+        raise ValueError("global_scale must be a contiguous float32 tensor of %d values" % B)
+    hh, dh = _norm_h(x, residual, h)
+    _same_device((x, out, sb, global_scale, hh))
+    dq = _desc(out, "out", packed=True)
+    with _on_device(x):
+        check(lib.rms_norm_nvfp4(ctypes.byref(dx), dr, weight.data_ptr(), eps, amax.data_ptr(), dh, ctypes.byref(dq),
+                                 sb.data_ptr(), int(mma), global_scale.data_ptr(), None, _stream(x)),
+              "rms_norm_nvfp4")
+    return out, sb, global_scale, hh
+
+
+def rms_norm_fake_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                        format: str = "mxfp8", amax: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None):
+    """The norm with its output fake-quantised (BF16 values of the codes of
+    rms_norm_mxfp8 / rms_norm_nvfp4), for quantisation-aware training.
+    Returns (y, h, rstd float32 [.., M])."""
+    if format not in ("mxfp8", "nvfp4"):
+        raise ValueError("format must be 'mxfp8' or 'nvfp4', got %r" % (format,))
+    if (format == "nvfp4") != (amax is not None):
+        raise ValueError("amax is given exactly with format='nvfp4'")
+    dx, dr, B = _norm_inputs(x, weight, residual, amax)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    _check_dtype(out, (torch.bfloat16,), "out")
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    hh, dh = _norm_h(x, residual, h)
+    _same_device((x, out, hh))
+    dy = _desc(out, "out")
+    with _on_device(x):
+        if format == "mxfp8":
+            check(lib.rms_norm_mxfp8_fake_quant(ctypes.byref(dx), dr, weight.data_ptr(), eps, dh, ctypes.byref(dy),
+                                                rstd.data_ptr(), _stream(x)), "rms_norm_mxfp8_fake_quant")
+        else:
+            check(lib.rms_norm_nvfp4_fake_quant(ctypes.byref(dx), dr, weight.data_ptr(), eps, amax.data_ptr(), dh,
+                                                ctypes.byref(dy), rstd.data_ptr(), _stream(x)),
+                  "rms_norm_nvfp4_fake_quant")
+    return out, hh, rstd
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      dh: Optional[torch.Tensor] = None, dweight_dtype=torch.float32, need_dweight: bool = True,
+                      out: Optional[torch.Tensor] = None):
+    """Gradient of the residual RMS norm, straight through its quantiser:
+    (dx, dweight) from dy (of the output), dh (of h, optional) and the
+    forward's h and rstd.  dx is the gradient of x and of the residual;
+    dweight [D] is float32 or bfloat16, or None when not needed."""
+    if dweight_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dweight_dtype must be float32 or bfloat16")
+    for t, name in ((dy, "dy"), (h, "h")) + (((dh, "dh"),) if dh is not None else ()):
+        _check_dtype(t, (torch.bfloat16,), name)
+    _check_dtype(weight, (torch.bfloat16,), "weight")
+    if weight.dim() != 1 or weight.shape[0] != h.shape[-1] or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous 1-D tensor of %d values" % h.shape[-1])
+    if rstd.dtype != torch.float32 or not rstd.is_contiguous() or rstd.shape != h.shape[:-1]:
+        raise ValueError("rstd must be a contiguous float32 tensor %s" % (tuple(h.shape[:-1]),))
+    if out is None:
+        out = torch.empty(h.shape, dtype=torch.bfloat16, device=h.device)
+    _check_dtype(out, (torch.bfloat16,), "out")
+    _same_device((h, dy, weight, rstd, dh, out))
+    ddy, dhh, dx = _desc(dy, "dy"), _desc(h, "h"), _desc(out, "out")
+    ddh = ctypes.byref(_desc(dh, "dh")) if dh is not None else None
+    with _on_device(h):
+        dw = ws = None
+        if need_dweight:
+            dw = torch.empty(h.shape[-1], dtype=dweight_dtype, device=h.device)
+            n = int(lib.rms_norm_backward_workspace_size(ctypes.byref(dhh)))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=h.device)
+        check(lib.rms_norm_backward(ctypes.byref(ddy), ddh, ctypes.byref(dhh), weight.data_ptr(), rstd.data_ptr(),
+                                    ctypes.byref(dx), dw.data_ptr() if need_dweight else None,
+                                    int(dweight_dtype == torch.bfloat16), ws.data_ptr() if need_dweight else None,
+                                    ws.numel() if need_dweight else 0, _stream(h)), "rms_norm_backward")
+    return out, dw
+
+
+class _RMSNormSTE(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, format, amax, eps):
+        y, h, rstd = rms_norm_fake_quant(x, weight, residual, format, amax, eps)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.set_materialize_grads(False)
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        dx, dw = dh, None
+        if dy is not None:
+            dx, dw = rms_norm_backward(_last_contiguous(dy), h, weight, rstd,
+                                       dh=_last_contiguous(dh) if dh is not None else None,
+                                       dweight_dtype=torch.bfloat16, need_dweight=need_w)
+        return dx if need_x else None, dw, dx if need_r else None, None, None, None
+
+
+def _last_contiguous(g):
+    """A gradient in the layout the library reads: an expanded or transposed one is copied."""
+    ok = g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(s % 8 == 0 and s > 0 for s in g.stride()[:-1])
+    return g if ok and (g.dim() < 3 or g.stride(0) >= g.shape[1] * g.stride(1)) else g.contiguous()
+
+
+def rms_norm_fake_quant_ste(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                            format: str = "mxfp8", amax: Optional[torch.Tensor] = None, eps: float = 1e-6):
+    """rms_norm_fake_quant with its backward pass (the quantiser straight
+    through, verl NVFP4 QAT article 2.3).  Returns (y, h); h is x itself
+    without a residual."""
+    if residual is None:
+        return _RMSNormSTE.apply(x, weight, None, format, amax, eps), x
+    return _RMSNormSTE.apply(x, weight, residual, format, amax, eps)
 
 
 # ---------------------------------------------------------------- diagnostics

@@ -91,6 +91,14 @@ _SIG = {
     "pwq_mma_scale_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "pwq_scales_to_mma": (_S, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P]),
     "pwq_scales_from_mma": (_S, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P]),
+    "rms_norm_mxfp8": (_S, [_T, _T, _P, ctypes.c_double, _T, _T, _P, ctypes.c_int, _P, _P]),
+    "rms_norm_nvfp4": (_S, [_T, _T, _P, ctypes.c_double, _P, _T, _T, _P, ctypes.c_int, _P, _P, _P]),
+    "rms_norm_mxfp8_fake_quant": (_S, [_T, _T, _P, ctypes.c_double, _T, _T, _P, _P]),
+    "rms_norm_nvfp4_fake_quant": (_S, [_T, _T, _P, ctypes.c_double, _P, _T, _T, _P, _P]),
+    "rms_norm_backward_workspace_size": (ctypes.c_size_t, [_T]),
+    "rms_norm_backward": (_S, [_T, _T, _T, _P, _P, _T, _P, ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "mxfp8_matmul": (_S, [_T, _P, _T, _P, _T, _P]),
+    "nvfp4_matmul": (_S, [_T, _P, _P, _T, _P, _P, _T, _P]),
     "mxfp8_quant_grouped_mma": (_S, [ctypes.c_int, _T, _T, _PP, _P]),
     "nvfp4_quant_grouped_mma": (_S, [ctypes.c_int, _IP, _T, _T, _PP, _PP, _P, ctypes.c_size_t, _P]),
 }

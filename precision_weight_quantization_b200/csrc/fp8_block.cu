@@ -599,26 +599,6 @@ fp8_requant_tma_kernel(const __grid_constant__ RequantTmaArgs a) {
     }
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no
-// link-time dependency on libcuda).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled_fn() {
-    static EncodeTiledFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
 // Fills the per-tensor descriptor; returns the tensor's tile count.
 uint32_t fill_tile_tensor(TileTensor& T, const Job& j, bool quant, uint32_t tile_begin) {
     const View& q = quant ? j.out : j.in;
@@ -647,6 +627,19 @@ uint32_t fill_tile_tensor(TileTensor& T, const Job& j, bool quant, uint32_t tile
 }
 
 }  // namespace
+
+EncodeTiledFn encode_tiled_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
 
 cudaError_t read_and_clear_device_error(uint32_t* code) {
     uint32_t zero = 0u;

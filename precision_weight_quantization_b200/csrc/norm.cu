@@ -1,0 +1,480 @@
+// norm.cu -- root-mean-square norm with the residual's addition and a
+// block-scaled output, forward and backward: the step in front of every
+// quantised linear layer of the rollout and of quantisation-aware training
+// ("Low Precision RL", "Modes" 3 and 4; verl NVFP4 QAT article 2.2, 2.3).
+//
+//   h = bf16(fl(x + residual))                     (h = x without a residual)
+//   rstd = (sum_d h_d^2 / D + eps)^(-1/2)
+//   y = bf16(h rstd weight)                        (one rounding)
+//
+// and the output is MXFP8 or NVFP4 (amax given) of y, bit for bit what
+// mxfp8_quant / nvfp4_quant write for that y, or its dequantised BF16 value.
+// One launch reads x and the residual once and writes h and the codes once;
+// y never reaches memory.
+//
+// y is the BF16 nearest to the exact product, so that codes do not depend on
+// the order of a sum: the squares are summed in 64 bits, h * weight is exact
+// in FP32 (8 + 8 significant bits), and only a product that lies within two
+// FP32 units of a BF16 tie (5 in 65536 of them) is formed again in 64 bits.
+// That costs 1 FP64 operation and about 4 integer ones per element, hidden
+// behind HBM.
+#include <algorithm>
+
+#include "pwq_internal.h"
+
+namespace pwq {
+namespace {
+
+constexpr int kVec = 4;   // 8-element vectors per thread, all loaded before any is used
+
+enum class NormOut { kMxfp8, kNvfp4, kMxfp8Fake, kNvfp4Fake };
+
+struct NormArgs {
+    View x, res, h, out;         // res.ptr / h.ptr null without a residual
+    const uint4* weight;
+    double eps;
+    const float* amax;           // NVFP4: [batch]
+    float* gs;                   // NVFP4 codes: [batch]
+    uint8_t* scale;              // codes: block scales
+    float* rstd;                 // [batch * rows] or null
+    FastDiv rows;                // rows per batch slab
+    uint32_t total_rows;
+    int vecs;                    // D / 8
+    int s_cols;                  // scale columns per row
+    int sf_mma;                  // tile layout
+    uint32_t sf_ct;
+    int64_t sf_slab;
+    uint32_t row_ctas, pad_rows; // CTAs that own rows; padding rows of the tile layout per slab
+    uint64_t pad_words;          // 4-byte words of those rows over all slabs
+};
+
+// h^2 summed in 64 bits: the BF16 h widened to 64 bits by moving its
+// exponent and mantissa (a zero becomes 2^-127, which no sum notices beside eps).
+__device__ __forceinline__ double widen_bits(uint32_t f32_bits) {
+    return __hiloint2double((int)(((f32_bits & 0x7fffffffu) >> 3) + 0x38000000u), 0);
+}
+__device__ __forceinline__ double add_squares(double s, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double lo = widen_bits(w[i] << 16), hi = widen_bits(w[i] & 0xffff0000u);
+        s = __fma_rn(lo, lo, s);
+        s = __fma_rn(hi, hi, s);
+    }
+    return s;
+}
+
+__device__ __forceinline__ uint4 add_bf16(uint4 a, uint4 b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = pack_bf16x2(__fadd_rn(bf16_lo(x[i]), bf16_lo(y[i])), __fadd_rn(bf16_hi(x[i]), bf16_hi(y[i])));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A 64-bit value as FP32 that rounds to the same BF16: the nearest FP32,
+// moved off a BF16 tie towards the value where it is not the value itself.
+__device__ __forceinline__ float narrow_for_bf16(float h, float w, double rstd) {
+    const double t = __dmul_rn((double)h * (double)w, rstd);
+    const float f = __double2float_rn(t);
+    const double back = (double)f;
+    if ((__float_as_uint(f) & 0xffffu) != 0x8000u || back == t) return f;
+    return __uint_as_float(__float_as_uint(f) + (fabs(t) > fabs(back) ? 1u : 0xffffffffu));
+}
+
+// y = bf16(h rstd weight) of 8 elements; rh = fl(rstd).
+__device__ __forceinline__ uint4 normalise(uint4 hv, uint4 wv, float rh, double rstd) {
+    const uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, w[4] = {wv.x, wv.y, wv.z, wv.w};
+    float q[8];
+    bool near_tie = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = i & 1 ? bf16_hi(h[i >> 1]) : bf16_lo(h[i >> 1]);
+        const float b = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        q[i] = __fmul_rn(__fmul_rn(a, b), rh);
+        const uint32_t u = __float_as_uint(q[i]);
+        // within two FP32 units of a tie; or so small or large (2^-96, infinite) that a factor left the normal range
+        near_tie |= ((u - 0x7ffeu) & 0xffffu) <= 4u;
+        near_tie |= ((u & 0x7fffffffu) - 0x0f800000u) >= 0x70000000u;
+    }
+    if (near_tie) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[2 * i] = narrow_for_bf16(bf16_lo(h[i]), bf16_lo(w[i]), rstd);
+            q[2 * i + 1] = narrow_for_bf16(bf16_hi(h[i]), bf16_hi(w[i]), rstd);
+        }
+    }
+    return make_uint4(pack_bf16x2(q[0], q[1]), pack_bf16x2(q[2], q[3]), pack_bf16x2(q[4], q[5]),
+                      pack_bf16x2(q[6], q[7]));
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Block scales of one row: `word` (valid in the first lane of every four
+// blocks) holds four consecutive scale bytes, zero past the last column;
+// `byte` this block's own, written by the block's first lane in the dense layout.
+__device__ __forceinline__ void store_scale(const NormArgs& a, uint32_t r, uint32_t b, uint32_t m, int col,
+                                            bool block_lane, bool word_lane, uint32_t byte, uint32_t word) {
+    if (a.sf_mma) {
+        if (word_lane)
+            st_u32(a.scale + (int64_t)b * a.sf_slab + mma_scale_offset(m, (uint32_t)col, a.sf_ct), word);
+    } else if (block_lane) {
+        a.scale[(int64_t)r * a.s_cols + col] = (uint8_t)byte;
+    }
+}
+
+// kThreads threads per row, one row per CTA.  Four (MXFP8) or two (NVFP4)
+// neighbouring lanes hold a block: 16-byte loads stay coalesced and the
+// block maximum takes one or two shuffles.
+template <NormOut kOut, int kThreads>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr bool kMx = kOut == NormOut::kMxfp8 || kOut == NormOut::kMxfp8Fake;
+    constexpr bool kFake = kOut == NormOut::kMxfp8Fake || kOut == NormOut::kNvfp4Fake;
+    constexpr int kWarps = kThreads / 32;
+    if (!kFake && blockIdx.x >= a.row_ctas) {   // zero scales of the rows that pad the last band
+        for (uint64_t i = (uint64_t)(blockIdx.x - a.row_ctas) * kThreads + threadIdx.x; i < a.pad_words;
+             i += (uint64_t)(gridDim.x - a.row_ctas) * kThreads) {
+            const uint64_t row = i / a.sf_ct;
+            const uint32_t ct = (uint32_t)(i - row * a.sf_ct);
+            const uint32_t b = (uint32_t)(row / a.pad_rows), m = a.rows.d + (uint32_t)(row - (uint64_t)b * a.pad_rows);
+            st_u32(a.scale + (int64_t)b * a.sf_slab + mma_scale_offset(m, 4u * ct, a.sf_ct), 0u);
+        }
+        return;
+    }
+    __shared__ double part[kWarps];
+    const uint32_t r = blockIdx.x;
+    const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
+    const int lane = threadIdx.x & 31;
+    const char* x = a.x.ptr + (int64_t)b * a.x.bstride + (int64_t)m * a.x.rstride;
+    uint4 v[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int k = i * kThreads + (int)threadIdx.x;
+        v[i] = k < a.vecs ? ld_stream_v4(x + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (a.res.ptr) {
+        const char* res = a.res.ptr + (int64_t)b * a.res.bstride + (int64_t)m * a.res.rstride;
+        char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride;
+        uint4 u[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int k = i * kThreads + (int)threadIdx.x;
+            u[i] = k < a.vecs ? ld_stream_v4(res + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int k = i * kThreads + (int)threadIdx.x;
+            v[i] = add_bf16(v[i], u[i]);
+            if (k < a.vecs) st_v4(h + 16 * (int64_t)k, v[i]);
+        }
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+        if (i * kThreads + (int)threadIdx.x < a.vecs) s = add_squares(s, v[i]);
+    s = warp_sum(s);
+    if (kWarps > 1) {
+        if (lane == 0) part[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) s += part[i];   // the same order in every thread
+    }
+    const double rstd = 1.0 / sqrt(s / (double)(8 * a.vecs) + a.eps);
+    const float rf = (float)rstd;
+    const float rh = rf < 0x1p-100f ? 0.0f : rf;   // huge rows: every product takes the 64-bit path
+    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rf;
+
+    float gs = 0.0f, g6 = 0.0f, r6 = 0.0f;
+    bool fast6 = false;
+    if (!kMx) {
+        gs = __fdiv_rn(__ldg(a.amax + b), 2688.0f);
+        g6 = __fmul_rn(6.0f, gs);
+        r6 = __frcp_rn(g6);
+        fast6 = div_fast_ok(g6);
+        if (!kFake && m == 0 && threadIdx.x == 0) a.gs[b] = gs;
+    }
+    char* out = a.out.ptr + (int64_t)b * a.out.bstride + (int64_t)m * a.out.rstride;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        if (i * kThreads >= a.vecs) break;   // uniform: shuffles below take whole warps
+        const int k = i * kThreads + (int)threadIdx.x;
+        const bool on = k < a.vecs;
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (on) y = normalise(v[i], __ldg(a.weight + k), rh, rstd);
+        uint32_t mw = amax_word8(y);
+        mw = hmax_abs(mw, __shfl_xor_sync(0xffffffffu, mw, 1));
+        if (kMx) mw = hmax_abs(mw, __shfl_xor_sync(0xffffffffu, mw, 2));
+        mw &= 0x7fff7fffu;
+        const uint32_t amax = max(mw & 0xffffu, mw >> 16);
+        if (kMx) {
+            const int e = ue8m0_exponent(amax);
+            float q[8];
+            const float inv = exp2i(-e);
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                q[2 * j] = __fmul_rn(bf16_lo(w[j]), inv);
+                q[2 * j + 1] = __fmul_rn(bf16_hi(w[j]), inv);
+            }
+            const uint2 c = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+            if (kFake) {
+                if (on) st_v4(out + 16 * (int64_t)k, fp8_dequant8(c, exp2i(e)));
+            } else {
+                if (on) st_v2(out + 8 * (int64_t)k, c);
+                const uint32_t byte = on ? (uint32_t)(e + 127) : 0u;
+                uint32_t word = byte;
+#pragma unroll
+                for (int j = 1; j < 4; ++j) word |= __shfl_down_sync(0xffffffffu, byte, 4 * j) << (8 * j);
+                store_scale(a, r, b, m, k >> 2, on && (k & 3) == 0, on && (k & 15) == 0, byte, word);
+            }
+        } else {
+            const float am = __uint_as_float(amax << 16);
+            uint32_t sb = 0u;
+            if (gs != 0.0f) sb = e4m3x2(fast6 ? div_fast(am, g6, r6) : div_slow(am, g6), 0.0f) & 0xffu;
+            const float d = __fmul_rn(e4m3_decode(sb), gs);
+            float q[8];
+            if (div_fast_ok(d)) quotients8<true>(y, d, __frcp_rn(d), q);
+            else quotients8<false>(y, d, 0.0f, q);
+            const uint32_t c = e2m1x8(q);
+            if (kFake) {
+                if (on) st_v4(out + 16 * (int64_t)k, dequant_half(c, e4m3_decode(sb), gs));
+            } else {
+                if (on) st_u32(out + 4 * (int64_t)k, c);
+                const uint32_t byte = on ? sb : 0u;
+                uint32_t word = byte;
+#pragma unroll
+                for (int j = 1; j < 4; ++j) word |= __shfl_down_sync(0xffffffffu, byte, 2 * j) << (8 * j);
+                store_scale(a, r, b, m, k >> 1, on && (k & 1) == 0, on && (k & 7) == 0, byte, word);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward
+//
+// With g = dy weight, xhat = h rstd and c = sum_d g_d xhat_d / D:
+//   dx = bf16(rstd (g - c xhat) + dh)      (also the residual's gradient)
+//   dweight = sum over rows of dy xhat
+// (the quantiser passes its gradient straight through).  A CTA walks rows
+// blockIdx.x, + gridDim.x, ... and keeps its part of dweight in FP32
+// registers; the parts are added in CTA order by a second launch, so the
+// result does not depend on timing.  FP32 throughout: the inputs are BF16
+// and no value decides a code.
+
+struct NormBwdArgs {
+    View dy, dh, h, dx;          // dh.ptr null: no gradient of h
+    const uint4* weight;
+    const float* rstd;
+    float* parts;                // [gridDim.x][D], null: no dweight
+    FastDiv rows;
+    uint32_t total_rows;
+    int vecs;
+};
+
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float part[2][kWarps];
+    float dw[kVec][8];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    int flip = 0;
+    for (uint32_t r = blockIdx.x; r < a.total_rows; r += gridDim.x, flip ^= 1) {
+        const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
+        const char* dy = a.dy.ptr + (int64_t)b * a.dy.bstride + (int64_t)m * a.dy.rstride;
+        const char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride;
+        const char* dh = a.dh.ptr ? a.dh.ptr + (int64_t)b * a.dh.bstride + (int64_t)m * a.dh.rstride : nullptr;
+        char* dx = a.dx.ptr + (int64_t)b * a.dx.bstride + (int64_t)m * a.dx.rstride;
+        const float rstd = __ldg(a.rstd + r);
+        uint4 vg[kVec], vh[kVec], vd[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int k = i * kThreads + (int)threadIdx.x;
+            const bool on = k < a.vecs;
+            vg[i] = on ? ld_stream_v4(dy + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
+            vh[i] = on ? ld_stream_v4(h + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
+            vd[i] = on && dh ? ld_stream_v4(dh + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float c = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int k = i * kThreads + (int)threadIdx.x;
+            const uint4 wv = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
+            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float t0 = bf16_lo(g[j]) * (bf16_lo(hh[j]) * rstd), t1 = bf16_hi(g[j]) * (bf16_hi(hh[j]) * rstd);
+                dw[i][2 * j] += t0;
+                dw[i][2 * j + 1] += t1;
+                c = __fmaf_rn(t0, bf16_lo(w[j]), c);
+                c = __fmaf_rn(t1, bf16_hi(w[j]), c);
+            }
+        }
+        c = warp_sum_f(c);
+        if (kWarps > 1) {
+            if ((threadIdx.x & 31) == 0) part[flip][threadIdx.x >> 5] = c;
+            __syncthreads();   // one barrier a row: the two halves of `part` alternate
+            c = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) c += part[flip][i];
+        }
+        c = __fdiv_rn(c, (float)(8 * a.vecs));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int k = i * kThreads + (int)threadIdx.x;
+            if (k >= a.vecs) continue;
+            const uint4 wv = __ldg(a.weight + k);
+            const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
+            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w}, d[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e0 = __fmaf_rn(bf16_lo(hh[j]) * rstd, -c, bf16_lo(g[j]) * bf16_lo(w[j]));
+                const float e1 = __fmaf_rn(bf16_hi(hh[j]) * rstd, -c, bf16_hi(g[j]) * bf16_hi(w[j]));
+                o[j] = pack_bf16x2(__fmaf_rn(e0, rstd, bf16_lo(d[j])), __fmaf_rn(e1, rstd, bf16_hi(d[j])));
+            }
+            st_v4(dx + 16 * (int64_t)k, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+    if (a.parts) {
+        float* p = a.parts + (int64_t)blockIdx.x * a.vecs * 8;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int k = i * kThreads + (int)threadIdx.x;
+            if (k >= a.vecs) continue;
+            float* q = p + 8 * (int64_t)k;
+            st_v4(q, make_uint4(__float_as_uint(dw[i][0]), __float_as_uint(dw[i][1]), __float_as_uint(dw[i][2]),
+                                __float_as_uint(dw[i][3])));
+            st_v4(q + 4, make_uint4(__float_as_uint(dw[i][4]), __float_as_uint(dw[i][5]), __float_as_uint(dw[i][6]),
+                                    __float_as_uint(dw[i][7])));
+        }
+    }
+}
+
+// dweight[d] = sum of the parts in a fixed order: 8 warps take every eighth
+// part of 32 columns, then the 8 sums are added.
+__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* parts, int n_parts, int D, void* dweight,
+                                                           int bf16_out) {
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int d = (int)blockIdx.x * 32 + lane;
+    float v = 0.0f;
+    if (d < D)
+        for (int p = warp; p < n_parts; p += 8) v += __ldg(parts + (int64_t)p * D + d);
+    s[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && d < D) {
+        v = s[0][lane];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += s[i][lane];
+        if (bf16_out) static_cast<uint16_t*>(dweight)[d] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
+        else static_cast<float*>(dweight)[d] = v;
+    }
+}
+
+// Threads per row: the fewest that hold the row in kVec vectors each.
+int norm_threads(int64_t D) {
+    int t = 32;
+    while ((int64_t)t * kVec * 8 < D) t *= 2;
+    return t;
+}
+
+template <NormOut kOut>
+cudaError_t launch_norm_out(const NormArgs& a, int threads, cudaStream_t s) {
+    const unsigned pads = a.pad_words ? (unsigned)std::min<uint64_t>((a.pad_words + threads - 1) / threads, 128) : 0u;
+    const unsigned grid = a.row_ctas + pads;
+    switch (threads) {
+        case 32: norm_kernel<kOut, 32><<<grid, 32, 0, s>>>(a); break;
+        case 64: norm_kernel<kOut, 64><<<grid, 64, 0, s>>>(a); break;
+        case 128: norm_kernel<kOut, 128><<<grid, 128, 0, s>>>(a); break;
+        case 256: norm_kernel<kOut, 256><<<grid, 256, 0, s>>>(a); break;
+        case 512: norm_kernel<kOut, 512><<<grid, 512, 0, s>>>(a); break;
+        default: norm_kernel<kOut, 1024><<<grid, 1024, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+int norm_bwd_grid(int64_t rows, int threads) {
+    const int per_sm = std::max(1, std::min(16, 512 / threads));
+    return persistent_grid(rows, per_sm);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const Norm& n, cudaStream_t s) {
+    NormArgs a;
+    a.x = n.x;
+    a.res = n.res;
+    a.h = n.h;
+    a.out = n.out;
+    a.weight = static_cast<const uint4*>(n.weight);
+    a.eps = n.eps;
+    a.amax = n.amax;
+    a.gs = n.gs;
+    a.scale = n.scale;
+    a.rstd = n.rstd;
+    a.rows = make_fastdiv((uint32_t)n.x.rows);
+    a.total_rows = (uint32_t)(n.x.batch * n.x.rows);
+    a.vecs = (int)(n.x.cols / 8);
+    a.s_cols = (int)(n.x.cols / (n.fp4 ? 16 : 32));
+    a.sf_mma = n.scale_mma;
+    a.sf_ct = (uint32_t)mma_scale_col_tiles(a.s_cols);
+    a.sf_slab = mma_scale_slab_bytes(n.x.rows, a.s_cols);
+    a.row_ctas = a.total_rows;
+    a.pad_rows = n.scale_mma && !n.fake ? (uint32_t)((128 - n.x.rows % 128) % 128) : 0u;
+    a.pad_words = (uint64_t)n.x.batch * a.pad_rows * a.sf_ct;
+    const int threads = norm_threads(n.x.cols);
+    if (n.fp4) return n.fake ? launch_norm_out<NormOut::kNvfp4Fake>(a, threads, s)
+                             : launch_norm_out<NormOut::kNvfp4>(a, threads, s);
+    return n.fake ? launch_norm_out<NormOut::kMxfp8Fake>(a, threads, s)
+                  : launch_norm_out<NormOut::kMxfp8>(a, threads, s);
+}
+
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
+    return ((size_t)norm_bwd_grid(rows, norm_threads(D)) * (size_t)D * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
+    NormBwdArgs a;
+    a.dy = n.dy;
+    a.dh = n.dh;
+    a.h = n.h;
+    a.dx = n.dx;
+    a.weight = static_cast<const uint4*>(n.weight);
+    a.rstd = n.rstd;
+    a.parts = n.dweight ? static_cast<float*>(n.workspace) : nullptr;
+    a.rows = make_fastdiv((uint32_t)n.h.rows);
+    a.total_rows = (uint32_t)(n.h.batch * n.h.rows);
+    a.vecs = (int)(n.h.cols / 8);
+    const int threads = norm_threads(n.h.cols), grid = norm_bwd_grid(a.total_rows, threads);
+    switch (threads) {
+        case 32: norm_bwd_kernel<32><<<grid, 32, 0, s>>>(a); break;
+        case 64: norm_bwd_kernel<64><<<grid, 64, 0, s>>>(a); break;
+        case 128: norm_bwd_kernel<128><<<grid, 128, 0, s>>>(a); break;
+        case 256: norm_bwd_kernel<256><<<grid, 256, 0, s>>>(a); break;
+        case 512: norm_bwd_kernel<512><<<grid, 512, 0, s>>>(a); break;
+        default: norm_bwd_kernel<1024><<<grid, 1024, 0, s>>>(a); break;
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !n.dweight) return e;
+    const int D = (int)n.h.cols;
+    norm_dweight_kernel<<<(D + 31) / 32, 256, 0, s>>>(a.parts, grid, D, n.dweight, n.dweight_bf16);
+    return cudaGetLastError();
+}
+
+}  // namespace pwq

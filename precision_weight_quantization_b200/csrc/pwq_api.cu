@@ -76,7 +76,8 @@ pwq_status cuda_fail(cudaError_t e) {
 
 pwq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PWQ_OK : cuda_fail(e); }
 
-enum class Kind { kBF16, kByte, kPacked4 };
+// kBF16Any: BF16 stored element by element where its rows are not 16-byte aligned
+enum class Kind { kBF16, kBF16Any, kByte, kPacked4 };
 
 struct Extent {
     uintptr_t lo = 0, hi = 0;  // [lo, hi) in bytes; empty when lo == hi
@@ -103,7 +104,7 @@ pwq_status check_tensor(const pwq_tensor* t, Kind k, View* v, Extent* ext, const
     if (t->batch < 0 || t->rows < 0 || t->cols < 0 || t->batch > kMaxDim || t->rows > kMaxDim ||
         t->cols > kMaxDim)
         return fail(PWQ_ERR_SHAPE, name);
-    const int64_t unit = (k == Kind::kBF16) ? 2 : 1;
+    const int64_t unit = (k == Kind::kBF16 || k == Kind::kBF16Any) ? 2 : 1;
     const int64_t row_units = (k == Kind::kPacked4) ? (t->cols + 1) / 2 : t->cols;
     v->ptr = static_cast<char*>(t->ptr);
     v->batch = t->batch;
@@ -120,7 +121,7 @@ pwq_status check_tensor(const pwq_tensor* t, Kind k, View* v, Extent* ext, const
         return fail(PWQ_ERR_SHAPE, "tensor too large (more than 2^31 8-element chunks)");
     // BF16 rows are moved in 16-byte vectors (and by TMA); code rows in
     // 8-byte (E4M3) or 4-byte (packed E2M1) pieces
-    const int64_t align = (k == Kind::kBF16) ? 16 : 8;
+    const int64_t align = (k == Kind::kBF16) ? 16 : (k == Kind::kBF16Any) ? 2 : 8;
     if ((uintptr_t)t->ptr % align != 0 || (t->row_stride * unit) % align != 0 ||
         (t->batch > 1 && (t->batch_stride * unit) % align != 0))
         return fail(PWQ_ERR_ALIGN, name);
@@ -284,7 +285,10 @@ pwq_status pwq_device_error(uint32_t* code) {
     if (e != cudaSuccess) return cuda_fail(e);
     e = pwq::read_and_clear_flow_error(&b);
     if (e != cudaSuccess) return cuda_fail(e);
-    *code = a | b;
+    uint32_t c = 0;
+    e = pwq::read_and_clear_matmul_error(&c);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *code = a | b | c;
     return PWQ_OK;
 }
 
@@ -388,6 +392,236 @@ pwq_status nvfp4_dequant_grouped(int n, const pwq_tensor* q_packed, const uint8_
                                  const float* const* global_scale, const pwq_tensor* y, pwq_stream_t stream) {
     return run_list(Op::kNvDequant, n, q_packed, y, reinterpret_cast<void* const*>(const_cast<uint8_t**>(sb)),
                     global_scale, stream);
+}
+
+// ------------------------------------------------------------------ block-scaled products
+
+namespace {
+
+// Validates a product; *launch is false when there is nothing to launch
+// (an empty y, or an empty K, whose zeros are written here).
+pwq_status check_product(const pwq_tensor* a, const uint8_t* a_scale, const float* a_gs, const pwq_tensor* w,
+                         const uint8_t* w_scale, const float* w_gs, const pwq_tensor* y, bool fp4, pwq::Product* p,
+                         cudaStream_t s, bool* launch) {
+    *launch = false;
+    if (!a || !w || !y) return fail(PWQ_ERR_NULL, "tensor descriptor");
+    const int64_t block = fp4 ? 16 : 32;
+    if (a->cols % block != 0) return fail(PWQ_ERR_SHAPE, fp4 ? "K % 16 != 0" : "K % 32 != 0");
+    const Kind codes = fp4 ? Kind::kPacked4 : Kind::kByte;
+    Extent ea, ew, ey;
+    pwq_status st;
+    if ((st = check_tensor(a, codes, &p->a, &ea, "a")) != PWQ_OK) return st;
+    if ((st = check_tensor(w, codes, &p->w, &ew, "w")) != PWQ_OK) return st;
+    if ((st = check_tensor(y, Kind::kBF16Any, &p->y, &ey, "y")) != PWQ_OK) return st;
+    if (a->batch != w->batch || a->batch != y->batch || a->cols != w->cols || y->rows != a->rows ||
+        y->cols != w->rows)
+        return fail(PWQ_ERR_SHAPE, "a [B][M][K], w [B][N][K], y [B][M][N] expected");
+    if (empty(y)) return PWQ_OK;
+    if (a->cols == 0) {
+        for (int64_t b = 0; b < y->batch; ++b) {
+            const cudaError_t e = cudaMemset2DAsync(p->y.ptr + b * p->y.bstride, (size_t)p->y.rstride, 0,
+                                                    (size_t)y->cols * 2, (size_t)y->rows, s);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        return PWQ_OK;
+    }
+    const pwq_tensor* operands[2] = {a, w};
+    for (const pwq_tensor* t : operands)
+        if ((uintptr_t)t->ptr % 16 != 0 || t->row_stride % 16 != 0 || (t->batch > 1 && t->batch_stride % 16 != 0))
+            return fail(PWQ_ERR_ALIGN, "a product's code rows are 16-byte aligned");
+    if (!a_scale || !w_scale) return fail(PWQ_ERR_NULL, "scale array");
+    if ((uintptr_t)a_scale % 16 != 0 || (uintptr_t)w_scale % 16 != 0)
+        return fail(PWQ_ERR_ALIGN, "tile-layout scales are 16-byte aligned");
+    if (fp4 && (!a_gs || !w_gs)) return fail(PWQ_ERR_NULL, "global_scale");
+    if (fp4 && ((uintptr_t)a_gs % 4 != 0 || (uintptr_t)w_gs % 4 != 0)) return fail(PWQ_ERR_ALIGN, "global_scale");
+    // tiles of one launch are numbered in 31 bits
+    if (a->batch * ceil_div(a->rows, 16) > ((int64_t)1 << 27) / ceil_div(w->rows, 128))
+        return fail(PWQ_ERR_SHAPE, "product too large (more than 2^27 output tiles)");
+    const int64_t B = a->batch, sc = a->cols / block;
+    const Extent ins[6] = {ea, ew, extent_of(a_scale, (size_t)(B * pwq::mma_scale_slab_bytes(a->rows, sc))),
+                           extent_of(w_scale, (size_t)(B * pwq::mma_scale_slab_bytes(w->rows, sc))),
+                           extent_of(a_gs, fp4 ? (size_t)B * 4 : 0), extent_of(w_gs, fp4 ? (size_t)B * 4 : 0)};
+    if ((st = check_overlaps(ins, 6, &ey, 1)) != PWQ_OK) return st;
+    p->a_scale = a_scale;
+    p->w_scale = w_scale;
+    p->a_gs = fp4 ? a_gs : nullptr;
+    p->w_gs = fp4 ? w_gs : nullptr;
+    p->k = a->cols;
+    *launch = true;
+    return PWQ_OK;
+}
+
+}  // namespace
+
+pwq_status mxfp8_matmul(const pwq_tensor* a, const uint8_t* a_scale_mma, const pwq_tensor* w,
+                        const uint8_t* w_scale_mma, const pwq_tensor* y, pwq_stream_t stream) {
+    pwq::Product p;
+    bool launch;
+    const pwq_status st = check_product(a, a_scale_mma, nullptr, w, w_scale_mma, nullptr, y, false, &p,
+                                        (cudaStream_t)stream, &launch);
+    if (st != PWQ_OK || !launch) return st;
+    return from_cuda(pwq::launch_mxfp8_matmul(p, (cudaStream_t)stream));
+}
+
+pwq_status nvfp4_matmul(const pwq_tensor* a_packed, const uint8_t* a_sb_mma, const float* a_global_scale,
+                        const pwq_tensor* w_packed, const uint8_t* w_sb_mma, const float* w_global_scale,
+                        const pwq_tensor* y, pwq_stream_t stream) {
+    pwq::Product p;
+    bool launch;
+    const pwq_status st = check_product(a_packed, a_sb_mma, a_global_scale, w_packed, w_sb_mma, w_global_scale, y,
+                                        true, &p, (cudaStream_t)stream, &launch);
+    if (st != PWQ_OK || !launch) return st;
+    return from_cuda(pwq::launch_nvfp4_matmul(p, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ residual RMS norm
+
+namespace {
+
+struct NormOutputs {
+    const pwq_tensor* out;
+    uint8_t* scale;      // codes
+    int scale_mma;
+    const float* amax;   // NVFP4
+    float* gs;           // NVFP4 codes
+};
+
+pwq_status run_norm(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                    const pwq_tensor* h, const NormOutputs& o, float* rstd, bool fp4, bool fake, cudaStream_t s) {
+    if (!x || !o.out) return fail(PWQ_ERR_NULL, "tensor descriptor");
+    if ((residual != nullptr) != (h != nullptr)) return fail(PWQ_ERR_ARG, "h is given exactly with a residual");
+    if (!(eps >= 1e-16 && eps <= 1e30)) return fail(PWQ_ERR_ARG, "eps outside [1e-16, 1e30]");
+    if (o.scale_mma != 0 && o.scale_mma != 1) return fail(PWQ_ERR_ARG, "scale_mma is 0 or 1");
+    pwq::Norm n = {};
+    Extent ex, er, eh, eo;
+    pwq_status st;
+    if ((st = check_tensor(x, Kind::kBF16, &n.x, &ex, "x")) != PWQ_OK) return st;
+    if ((st = check_tensor(o.out, fake ? Kind::kBF16 : fp4 ? Kind::kPacked4 : Kind::kByte, &n.out, &eo, "output")) !=
+        PWQ_OK)
+        return st;
+    if (!same_shape(x, o.out)) return fail(PWQ_ERR_SHAPE, "output shape != input shape");
+    if (residual) {
+        if ((st = check_tensor(residual, Kind::kBF16, &n.res, &er, "residual")) != PWQ_OK) return st;
+        if ((st = check_tensor(h, Kind::kBF16, &n.h, &eh, "h")) != PWQ_OK) return st;
+        if (!same_shape(x, residual) || !same_shape(x, h)) return fail(PWQ_ERR_SHAPE, "residual / h shape != x shape");
+    }
+    const int64_t block = fp4 ? 16 : 32;
+    if (x->cols % block != 0) return fail(PWQ_ERR_SHAPE, fp4 ? "cols % 16 != 0" : "cols % 32 != 0");
+    if (x->cols > pwq::kMaxNormCols) return fail(PWQ_ERR_SHAPE, "more than 32768 columns");
+    if (x->batch * x->rows > kMaxChunks) return fail(PWQ_ERR_SHAPE, "too many rows");
+    if (empty(x)) return PWQ_OK;
+    if (!weight) return fail(PWQ_ERR_NULL, "weight");
+    if ((uintptr_t)weight % 16 != 0) return fail(PWQ_ERR_ALIGN, "weight");
+    if (fp4 && !o.amax) return fail(PWQ_ERR_NULL, "amax_in");
+    if (fp4 && (uintptr_t)o.amax % 4 != 0) return fail(PWQ_ERR_ALIGN, "amax_in");
+    if (!fake && !o.scale) return fail(PWQ_ERR_NULL, "scale");
+    if (!fake && o.scale_mma && (uintptr_t)o.scale % 4 != 0) return fail(PWQ_ERR_ALIGN, "tile-layout scales");
+    if (!fake && fp4 && !o.gs) return fail(PWQ_ERR_NULL, "global_scale");
+    if (!fake && fp4 && (uintptr_t)o.gs % 4 != 0) return fail(PWQ_ERR_ALIGN, "global_scale");
+    if ((uintptr_t)rstd % 4 != 0) return fail(PWQ_ERR_ALIGN, "rstd");
+    // h may be x or the residual exactly (in place); every other overlap is an error
+    const bool h_is_x = residual && exact_alias(h, x), h_is_r = residual && exact_alias(h, residual);
+    const int64_t B = x->batch, sc = x->cols / block;
+    const Extent none{};
+    const Extent ins[4] = {h_is_x ? none : ex, residual && !h_is_r ? er : none,
+                           extent_of(weight, (size_t)x->cols * 2), extent_of(o.amax, fp4 ? (size_t)B * 4 : 0)};
+    const Extent outs[5] = {eo, residual ? eh : none,
+                            extent_of(o.scale, fake ? 0
+                                               : o.scale_mma
+                                                   ? (size_t)(B * pwq::mma_scale_slab_bytes(x->rows, sc))
+                                                   : (size_t)(B * x->rows * sc)),
+                            extent_of(o.gs, fp4 && !fake ? (size_t)B * 4 : 0),
+                            extent_of(rstd, rstd ? (size_t)(B * x->rows) * 4 : 0)};
+    if ((st = check_overlaps(ins, 4, outs, 5)) != PWQ_OK) return st;
+    // an in-place h still excludes its input from the other outputs: its extent is an output above
+    n.weight = weight;
+    n.eps = eps;
+    n.fp4 = fp4;
+    n.fake = fake;
+    n.amax = o.amax;
+    n.gs = o.gs;
+    n.scale = o.scale;
+    n.scale_mma = o.scale_mma;
+    n.rstd = rstd;
+    return from_cuda(pwq::launch_norm(n, s));
+}
+
+}  // namespace
+
+pwq_status rms_norm_mxfp8(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                          const pwq_tensor* h, const pwq_tensor* q, uint8_t* scale, int scale_mma, float* rstd,
+                          pwq_stream_t stream) {
+    return run_norm(x, residual, weight, eps, h, {q, scale, scale_mma, nullptr, nullptr}, rstd, false, false,
+                    (cudaStream_t)stream);
+}
+
+pwq_status rms_norm_nvfp4(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                          const float* amax_in, const pwq_tensor* h, const pwq_tensor* q_packed, uint8_t* sb,
+                          int sb_mma, float* global_scale, float* rstd, pwq_stream_t stream) {
+    return run_norm(x, residual, weight, eps, h, {q_packed, sb, sb_mma, amax_in, global_scale}, rstd, true, false,
+                    (cudaStream_t)stream);
+}
+
+pwq_status rms_norm_mxfp8_fake_quant(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                                     const pwq_tensor* h, const pwq_tensor* y, float* rstd, pwq_stream_t stream) {
+    return run_norm(x, residual, weight, eps, h, {y, nullptr, 0, nullptr, nullptr}, rstd, false, true,
+                    (cudaStream_t)stream);
+}
+
+pwq_status rms_norm_nvfp4_fake_quant(const pwq_tensor* x, const pwq_tensor* residual, const void* weight, double eps,
+                                     const float* amax_in, const pwq_tensor* h, const pwq_tensor* y, float* rstd,
+                                     pwq_stream_t stream) {
+    return run_norm(x, residual, weight, eps, h, {y, nullptr, 0, amax_in, nullptr}, rstd, true, true,
+                    (cudaStream_t)stream);
+}
+
+size_t rms_norm_backward_workspace_size(const pwq_tensor* h) {
+    if (!h || h->batch < 0 || h->rows < 0 || h->cols < 0 || h->cols > pwq::kMaxNormCols || h->batch > kMaxDim ||
+        h->rows > kMaxDim)
+        return 0;
+    return pwq::norm_bwd_workspace_bytes(std::max<int64_t>(1, h->batch * h->rows), std::max<int64_t>(8, h->cols));
+}
+
+pwq_status rms_norm_backward(const pwq_tensor* dy, const pwq_tensor* dh, const pwq_tensor* h, const void* weight,
+                             const float* rstd, const pwq_tensor* dx, void* dweight, int dweight_bf16,
+                             void* workspace, size_t workspace_bytes, pwq_stream_t stream) {
+    if (!dy || !h || !dx) return fail(PWQ_ERR_NULL, "tensor descriptor");
+    if (dweight_bf16 != 0 && dweight_bf16 != 1) return fail(PWQ_ERR_ARG, "dweight_bf16 is 0 or 1");
+    pwq::NormBwd n = {};
+    Extent ey, ed, eh, ex;
+    pwq_status st;
+    if ((st = check_tensor(dy, Kind::kBF16, &n.dy, &ey, "dy")) != PWQ_OK) return st;
+    if ((st = check_tensor(h, Kind::kBF16, &n.h, &eh, "h")) != PWQ_OK) return st;
+    if ((st = check_tensor(dx, Kind::kBF16, &n.dx, &ex, "dx")) != PWQ_OK) return st;
+    if (dh && (st = check_tensor(dh, Kind::kBF16, &n.dh, &ed, "dh")) != PWQ_OK) return st;
+    if (!same_shape(h, dy) || !same_shape(h, dx) || (dh && !same_shape(h, dh)))
+        return fail(PWQ_ERR_SHAPE, "dy, dh, h and dx differ in shape");
+    if (h->cols % 16 != 0) return fail(PWQ_ERR_SHAPE, "cols % 16 != 0");
+    if (h->cols > pwq::kMaxNormCols) return fail(PWQ_ERR_SHAPE, "more than 32768 columns");
+    if (h->batch * h->rows > kMaxChunks) return fail(PWQ_ERR_SHAPE, "too many rows");
+    const size_t dw_bytes = dweight ? (size_t)h->cols * (dweight_bf16 ? 2 : 4) : 0;
+    if (dweight && (uintptr_t)dweight % (dweight_bf16 ? 2 : 4) != 0) return fail(PWQ_ERR_ALIGN, "dweight");
+    if (empty(h)) {   // the sum over no rows
+        if (dw_bytes == 0) return PWQ_OK;
+        return from_cuda(cudaMemsetAsync(dweight, 0, dw_bytes, (cudaStream_t)stream));
+    }
+    if (!weight) return fail(PWQ_ERR_NULL, "weight");
+    if (!rstd) return fail(PWQ_ERR_NULL, "rstd");
+    if ((uintptr_t)weight % 16 != 0) return fail(PWQ_ERR_ALIGN, "weight");
+    if ((uintptr_t)rstd % 4 != 0) return fail(PWQ_ERR_ALIGN, "rstd");
+    const size_t need = dweight ? pwq::norm_bwd_workspace_bytes(h->batch * h->rows, h->cols) : 0;
+    if (dweight && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need))
+        return fail(PWQ_ERR_WORKSPACE, "workspace missing, misaligned or too small");
+    const Extent ins[5] = {ey, dh ? ed : Extent{}, eh, extent_of(weight, (size_t)h->cols * 2),
+                           extent_of(rstd, (size_t)(h->batch * h->rows) * 4)};
+    const Extent outs[3] = {ex, extent_of(dweight, dw_bytes), extent_of(workspace, need)};
+    if ((st = check_overlaps(ins, 5, outs, 3)) != PWQ_OK) return st;
+    n.weight = weight;
+    n.rstd = rstd;
+    n.dweight = dweight;
+    n.dweight_bf16 = dweight_bf16;
+    n.workspace = workspace;
+    return from_cuda(pwq::launch_norm_bwd(n, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------------------ NVFP4 quantise / fake-quantise

@@ -450,6 +450,7 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
 
 // Bits of the device error word set by kernels whose bounded waits give up.
 constexpr uint32_t kErrTmaTimeout = 1u;
+constexpr uint32_t kErrMatmulTimeout = 4u;
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;

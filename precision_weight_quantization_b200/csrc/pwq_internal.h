@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "pwq_device.cuh"
@@ -26,6 +27,14 @@ int current_device();
 // flags are read and written under one lock.
 constexpr int kMaxDevices = 64;
 cudaError_t set_smem_limit_once(int* done, const void* const* fns, int n, int bytes);
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no
+// link-time dependency on libcuda); null when the driver lacks it.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();
 
 // Grid size for a persistent elementwise kernel: enough CTAs to cover
 // `work_ctas`, at most `per_sm` resident CTAs per SM.
@@ -154,6 +163,51 @@ cudaError_t read_and_clear_flow_error(uint32_t* code);
 // amax_out / gs_out (nullable) = A and fl(A / 2688).  words: 2 scratch words.
 cudaError_t launch_activation_observe(const View& x, int kind, float c, float* state, float* amax_out,
                                       float* gs_out, uint32_t* words, cudaStream_t s);
+
+// Block-scaled product y = a w^T (matmul.cu): code views (cols = K, row
+// strides and bases 16-byte aligned), tile-layout scales (16-byte aligned),
+// for NVFP4 the FP32 global scales [batch] of each operand, y BF16 (2-byte
+// aligned).  Non-empty operands; k = a.cols = w.cols.
+struct Product {
+    View a, w, y;
+    const uint8_t *a_scale, *w_scale;
+    const float *a_gs, *w_gs;   // null for MXFP8
+    int64_t k;
+};
+cudaError_t launch_mxfp8_matmul(const Product& p, cudaStream_t s);
+cudaError_t launch_nvfp4_matmul(const Product& p, cudaStream_t s);
+cudaError_t read_and_clear_matmul_error(uint32_t* code);
+
+// Residual RMS norm with a block-scaled (or fake-quantised BF16) output
+// (norm.cu), at most kMaxNormCols columns: x, res, h, out [B][M][D] views
+// (res.ptr / h.ptr null without a residual; h may be x or res exactly),
+// weight BF16 [D] 16-byte aligned, scale dense or in the tile layout.
+constexpr int64_t kMaxNormCols = 32768;
+struct Norm {
+    View x, res, h, out;
+    const void* weight;
+    double eps;
+    bool fp4, fake;
+    const float* amax;   // NVFP4: [B]
+    float* gs;           // NVFP4 codes: [B]
+    uint8_t* scale;      // codes
+    int scale_mma;
+    float* rstd;         // [B][M] or null
+};
+cudaError_t launch_norm(const Norm& n, cudaStream_t s);
+
+// Its backward pass; dh.ptr null without a gradient of h, dweight null when
+// not wanted (then workspace is unused), FP32 or BF16 [D].
+struct NormBwd {
+    View dy, dh, h, dx;
+    const void* weight;
+    const float* rstd;
+    void* dweight;
+    int dweight_bf16;
+    void* workspace;
+};
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s);
 
 cudaError_t launch_selftest_division(int which, unsigned long long* counts, cudaStream_t s);
 cudaError_t launch_selftest_codecs(uint32_t first, uint32_t count, uint8_t* e4m3, uint8_t* e2m1,

@@ -1,0 +1,160 @@
+// pwq_tcgen05.cuh -- 5th-generation tensor core helpers (sm_100a): tensor
+// memory, shared-memory matrix descriptors, block-scaled MMA and the scale
+// copies, as the PTX ISA's tcgen05 chapter defines them.
+#pragma once
+
+#include "pwq_device.cuh"
+
+namespace pwq {
+
+// ---------------------------------------------------------------- tensor memory
+
+// Whole warp.  Writes the TMEM base address of `cols` columns (a power of
+// two, 32..512) to the shared-memory word at `dst`.
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+    if (kCtas == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(dst), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+    if (kCtas == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(cols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(cols));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Whole warp: 16 / 32 consecutive 32-bit columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- descriptors
+
+// K-major operand tile in shared memory, rows of 128 bytes in the 128-byte
+// swizzle (1024-byte aligned, 8-row groups 1024 bytes apart).  Advancing
+// along K by 32 bytes inside the swizzled row adds 2 to the start address.
+__device__ __forceinline__ uint64_t desc_swizzle128(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+// A scale tile: 32 lines of 16 contiguous bytes, no swizzle (8-line groups
+// 128 bytes apart).
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// ---------------------------------------------------------------- formats of a block-scaled product
+
+// MXFP8: E4M3 codes, K = 32 per MMA (32 bytes), one UE8M0 byte per row and
+// MMA; a scale tile (four scale columns) serves the four MMAs of a 128-byte
+// step.  NVFP4: packed E2M1, K = 64 per MMA (32 bytes), four E4M3 bytes per
+// row and MMA; one scale tile per MMA.
+enum class ProductFormat { kMxfp8, kNvfp4 };
+
+template <ProductFormat kF>
+struct ProductTraits {
+    static constexpr bool kFp4 = kF == ProductFormat::kNvfp4;
+    static constexpr int kScaleTiles = kFp4 ? 4 : 1;     // 512-byte scale tiles per operand band and 128-byte step
+    static constexpr uint32_t kScaleBytes = 512u * kScaleTiles;
+};
+
+constexpr uint32_t kStepBytes = 128;   // bytes of a code row per pipeline step
+constexpr int kMmasPerStep = 4;        // 32 bytes of K each
+
+// Instruction descriptor for an M x N block-scaled MMA, FP32 accumulation,
+// both operands K-major.  MXFP8: scale format UE8M0 (bit 23), E4M3 (type 0);
+// NVFP4: scale format UE4M3, E2M1 (type 1 in bits 7 and 10).
+template <ProductFormat kF>
+__device__ constexpr uint32_t mma_idesc(int m, int n) {
+    return (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 7) << 27 |
+           (kF == ProductFormat::kNvfp4 ? (1u << 7 | 1u << 10) : 1u << 23);
+}
+
+// One thread.  D[tmem] (+)= A B^T with block scales; scale_a / scale_b are
+// the TMEM addresses of the scale tiles.
+template <ProductFormat kF, int kCtas>
+__device__ __forceinline__ void mma_block_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t scale_a,
+                                                 uint32_t scale_b, bool accumulate) {
+    const uint32_t acc = accumulate ? 1u : 0u;
+#define PWQ_MMA(GROUP, KIND)                                                                                     \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                               \
+                 "tcgen05.mma.cta_group::" GROUP "." KIND " [%0], %1, %2, %3, [%5], [%6], p;\n\t}"               \
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(scale_a), "r"(scale_b) : "memory")
+    if (kF == ProductFormat::kNvfp4) {
+        if (kCtas == 1) PWQ_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+        else PWQ_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    } else {
+        if (kCtas == 1) PWQ_MMA("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+        else PWQ_MMA("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    }
+#undef PWQ_MMA
+}
+
+// One thread: a 512-byte scale tile from shared memory into four TMEM
+// columns, repeated for the four warps' lanes.  Executed in order with the
+// MMAs that the same thread issues after it.
+template <int kCtas>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    if (kCtas == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
+}
+
+// One thread: arrives on `bar` when every tcgen05 operation issued by this
+// thread so far has completed.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster (warps converged).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared-memory address `addr` of this CTA, as seen in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+}  // namespace pwq
