@@ -12,7 +12,6 @@ Functions take CUDA tensors ([M, N] or batched [B, M, N], last dimension
 contiguous) and return newly allocated outputs unless ``out=`` buffers are
 given.  Nothing synchronises.
 """
-import contextlib
 import ctypes
 from typing import List, Optional, Sequence, Tuple
 
@@ -41,14 +40,9 @@ def _stream(t: torch.Tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-def _bmn(t: torch.Tensor, name: str):
-    if t.dim() == 2:
-        M, N = t.shape
-        return 1, M, N, M * t.stride(0), t.stride(0)
-    if t.dim() == 3:
-        B, M, N = t.shape
-        return B, M, N, t.stride(0), t.stride(1)
-    raise ValueError("%s must be 2-D [M, N] or 3-D [B, M, N], got shape %s" % (name, tuple(t.shape)))
+# The current stream's handle without making a Stream object (2 us less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _desc(t: torch.Tensor, name: str, packed: bool = False) -> PwqTensor:
@@ -56,13 +50,22 @@ def _desc(t: torch.Tensor, name: str, packed: bool = False) -> PwqTensor:
     (uint8, two per byte) the logical column count is twice the byte count."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    B, M, N, bs, rs = _bmn(t, name)
-    if t.numel() == 0:
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        M, N = shape
+        B, bs, rs, last = 1, M * st[0], st[0], st[1]
+    elif len(shape) == 3:
+        B, M, N = shape
+        bs, rs, last = st
+    else:
+        raise ValueError("%s must be 2-D [M, N] or 3-D [B, M, N], got shape %s" % (name, tuple(shape)))
+    cols = 2 * N if packed else N
+    if B == 0 or M == 0 or N == 0:
         # an empty tensor's strides are arbitrary; the library launches nothing for it
-        return PwqTensor(t.data_ptr(), B, M, 2 * N if packed else N, M * N, N)
-    if N > 1 and t.stride(-1) != 1:
+        return PwqTensor(t.data_ptr(), B, M, cols, M * N, N)
+    if N > 1 and last != 1:
         raise ValueError("%s: last dimension must be contiguous" % name)
-    return PwqTensor(t.data_ptr(), B, M, 2 * N if packed else N, bs, rs)
+    return PwqTensor(t.data_ptr(), B, M, cols, bs, rs)
 
 
 def _lead(x: torch.Tensor):
@@ -577,36 +580,52 @@ def nvfp4_quant_grouped_mma(groups: Sequence[Sequence[torch.Tensor]], out=None, 
 
 # ---------------------------------------------------------------- block-scaled products
 
-def _same_device(ts):
-    dev = ts[0].device
-    for t in ts[1:]:
+def _launch(t: torch.Tensor, name: str, *args):
+    """Calls the library on t's device and its current stream (the library launches on the current device)."""
+    index = t.device.index
+    if torch.cuda.current_device() == index:
+        status = getattr(lib, name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib, name)(*args, _raw_stream(index))
+    if status:
+        check(status, name)
+
+
+def _same_device(first, *others):
+    dev = first.device
+    for t in others:
         if t is not None and t.device != dev:
             raise ValueError("tensors on different devices: %s and %s" % (dev, t.device))
 
 
-def _on_device(t: torch.Tensor):
-    """Makes t's device current for a call (the library launches on the current device)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+def _tile_bytes(B: int, rows: int, cols: int) -> int:
+    """mma_scale_bytes without the call."""
+    return B * -(-rows // 128) * -(-cols // 4) * 512
 
 
-def _mma_scales(scale: torch.Tensor, B: int, rows: int, cols: int, name: str) -> torch.Tensor:
-    n = B * -(-rows // 128) * -(-cols // 4) * 512
-    if scale.element_size() != 1 or not scale.is_contiguous() or scale.numel() != n:
-        raise ValueError("%s must be a contiguous one-byte tensor of the %d bytes of the tile layout (scales_to_mma)"
-                         % (name, n))
-    return scale
+def _one_byte(t: torch.Tensor, n: int, name: str, layout: str) -> int:
+    """Address of a contiguous one-byte tensor of n values."""
+    if t.element_size() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous one-byte tensor of the %d bytes of the %s layout"
+                         % (name, n, layout))
+    return t.data_ptr()
 
 
-def _product(a, w, out, fp4):
-    per = 2 if fp4 else 1
+def _floats(t: torch.Tensor, n: int, name: str) -> int:
+    """Address of a contiguous float32 tensor of n values."""
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of %d values" % (name, n))
+    return t.data_ptr()
+
+
+def _product_out(a, w, out):
     if a.dim() != w.dim():
         raise ValueError("a and w must both be 2-D or both 3-D, got %s and %s" % (tuple(a.shape), tuple(w.shape)))
-    B, M, K = _batch(a), a.shape[-2], a.shape[-1] * per
-    N = w.shape[-2]
     if out is None:
-        out = torch.empty(a.shape[:-1] + (N,), dtype=torch.bfloat16, device=a.device)
+        return torch.empty(a.shape[:-1] + (w.shape[-2],), dtype=torch.bfloat16, device=a.device)
     _check_dtype(out, (torch.bfloat16,), "out")
-    return B, M, N, K, out
+    return out
 
 
 def mxfp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -619,13 +638,13 @@ def mxfp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
     are not differentiable."""
     _check_dtype(a, _CODE_DTYPES, "a")
     _check_dtype(w, _CODE_DTYPES, "w")
-    B, M, N, K, out = _product(a, w, out, False)
-    _same_device((a, a_scale, w, w_scale, out))
+    out = _product_out(a, w, out)
+    _same_device(a, a_scale, w, w_scale, out)
     da, dw, dy = _desc(a, "a"), _desc(w, "w"), _desc(out, "out")
-    sa, sw = _mma_scales(a_scale, B, M, K // 32, "a_scale"), _mma_scales(w_scale, B, N, K // 32, "w_scale")
-    with _on_device(a):
-        check(lib.mxfp8_matmul(ctypes.byref(da), sa.data_ptr(), ctypes.byref(dw), sw.data_ptr(), ctypes.byref(dy),
-                               _stream(a)), "mxfp8_matmul")
+    S = da.cols // 32
+    _launch(a, "mxfp8_matmul", ctypes.byref(da), _one_byte(a_scale, _tile_bytes(da.batch, da.rows, S), "a_scale", "tile"),
+            ctypes.byref(dw), _one_byte(w_scale, _tile_bytes(da.batch, dw.rows, S), "w_scale", "tile"),
+            ctypes.byref(dy))
     return out
 
 
@@ -638,46 +657,35 @@ def nvfp4_matmul(a: torch.Tensor, a_sb: torch.Tensor, a_global_scale: torch.Tens
     scales [B].  As mxfp8_matmul otherwise."""
     _check_dtype(a, (torch.uint8,), "a")
     _check_dtype(w, (torch.uint8,), "w")
-    B, M, N, K, out = _product(a, w, out, True)
-    _same_device((a, a_sb, a_global_scale, w, w_sb, w_global_scale, out))
+    out = _product_out(a, w, out)
+    _same_device(a, a_sb, a_global_scale, w, w_sb, w_global_scale, out)
     da, dw, dy = _desc(a, "a", True), _desc(w, "w", True), _desc(out, "out")
-    sa, sw = _mma_scales(a_sb, B, M, K // 16, "a_sb"), _mma_scales(w_sb, B, N, K // 16, "w_sb")
-    for g, name in ((a_global_scale, "a_global_scale"), (w_global_scale, "w_global_scale")):
-        if g.dtype != torch.float32 or not g.is_contiguous() or g.numel() != B:
-            raise ValueError("%s must be a contiguous float32 tensor of %d values" % (name, B))
-    with _on_device(a):
-        check(lib.nvfp4_matmul(ctypes.byref(da), sa.data_ptr(), a_global_scale.data_ptr(), ctypes.byref(dw),
-                               sw.data_ptr(), w_global_scale.data_ptr(), ctypes.byref(dy), _stream(a)),
-              "nvfp4_matmul")
+    B, S = da.batch, da.cols // 16
+    _launch(a, "nvfp4_matmul", ctypes.byref(da), _one_byte(a_sb, _tile_bytes(B, da.rows, S), "a_sb", "tile"),
+            _floats(a_global_scale, B, "a_global_scale"), ctypes.byref(dw),
+            _one_byte(w_sb, _tile_bytes(B, dw.rows, S), "w_sb", "tile"),
+            _floats(w_global_scale, B, "w_global_scale"), ctypes.byref(dy))
     return out
 
 
 # ---------------------------------------------------------------- residual RMS norm with a block-scaled output
 
-def _norm_inputs(x, weight, residual, amax):
-    """Checks shared by the norms; returns (descriptor refs of x and residual, B)."""
+def _norm_inputs(x, weight, residual, h):
+    """Checks and descriptors shared by the norms: (x, residual and h descriptor references, x's descriptor, h)."""
     _check_dtype(x, (torch.bfloat16,), "x")
     _check_dtype(weight, (torch.bfloat16,), "weight")
-    B = _batch(x)
-    if weight.dim() != 1 or weight.shape[0] != x.shape[-1] or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous 1-D tensor of %d values" % x.shape[-1])
-    if residual is not None:
-        _check_dtype(residual, (torch.bfloat16,), "residual")
-    if amax is not None and (amax.dtype != torch.float32 or not amax.is_contiguous() or amax.numel() != B):
-        raise ValueError("amax must be a contiguous float32 tensor of %d values" % B)
-    _same_device((x, weight, residual, amax))
-    dr = ctypes.byref(_desc(residual, "residual")) if residual is not None else None
-    return _desc(x, "x"), dr, B
-
-
-def _norm_h(x, residual, h):
+    dx = _desc(x, "x")
+    if weight.dim() != 1 or weight.shape[0] != dx.cols or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous 1-D tensor of %d values" % dx.cols)
     if residual is None:
         if h is not None:
             raise ValueError("h is an output of the residual form only")
-        return x, None
-    h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if h is None else h
+        return ctypes.byref(dx), None, None, dx, x
+    _check_dtype(residual, (torch.bfloat16,), "residual")
+    if h is None:
+        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
     _check_dtype(h, (torch.bfloat16,), "h")
-    return h, ctypes.byref(_desc(h, "h"))
+    return ctypes.byref(dx), ctypes.byref(_desc(residual, "residual")), ctypes.byref(_desc(h, "h")), dx, h
 
 
 def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -689,25 +697,18 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     tensor-core tile layout (mma=True, for mxfp8_matmul) or dense
     [.., M, D/32]; h is x itself without a residual, and ``h=residual``
     updates the residual in place."""
-    dx, dr, B = _norm_inputs(x, weight, residual, None)
-    M, D = x.shape[-2:]
+    px, pr, ph, dx, h = _norm_inputs(x, weight, residual, h)
+    B, M, S = dx.batch, dx.rows, dx.cols // 32
+    n = _tile_bytes(B, M, S) if mma else B * M * S
     if out is None:
         out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    _check_dtype(out, _CODE_DTYPES, "out")
     if scale is None:
-        shape = (mma_scale_bytes(B, M, D // 32),) if mma else x.shape[:-1] + (D // 32,)
-        scale = torch.empty(shape, dtype=torch.uint8, device=x.device)
-    if mma:
-        _mma_scales(scale, B, M, D // 32, "scale")
-    elif scale.element_size() != 1 or not scale.is_contiguous() or scale.numel() != B * M * (D // 32):
-        raise ValueError("scale must be a contiguous one-byte tensor [.., M, D/32]")
-    hh, dh = _norm_h(x, residual, h)
-    _same_device((x, out, scale, hh))
-    dq = _desc(out, "out")
-    with _on_device(x):
-        check(lib.rms_norm_mxfp8(ctypes.byref(dx), dr, weight.data_ptr(), eps, dh, ctypes.byref(dq),
-                                 scale.data_ptr(), int(mma), None, _stream(x)), "rms_norm_mxfp8")
-    return out, scale, hh
+        scale = torch.empty((n,) if mma else x.shape[:-1] + (S,), dtype=torch.uint8, device=x.device)
+    _check_dtype(out, _CODE_DTYPES, "out")
+    _same_device(x, weight, residual, out, scale, h)
+    _launch(x, "rms_norm_mxfp8", px, pr, weight.data_ptr(), eps, ph, ctypes.byref(_desc(out, "out")),
+            _one_byte(scale, n, "scale", "tile" if mma else "dense"), int(mma), None)
+    return out, scale, h
 
 
 def rms_norm_nvfp4(x: torch.Tensor, weight: torch.Tensor, amax: torch.Tensor,
@@ -717,30 +718,23 @@ def rms_norm_nvfp4(x: torch.Tensor, weight: torch.Tensor, amax: torch.Tensor,
     """rms_norm_mxfp8 with NVFP4 output for a given activation amax (float32
     [B], an NVFP4ActivationObserver's).  Returns (packed codes uint8
     [.., M, D/2], block scales, global scales float32 [B], h)."""
-    dx, dr, B = _norm_inputs(x, weight, residual, amax)
-    M, D = x.shape[-2:]
+    px, pr, ph, dx, h = _norm_inputs(x, weight, residual, h)
+    B, M, S = dx.batch, dx.rows, dx.cols // 16
+    n = _tile_bytes(B, M, S) if mma else B * M * S
+    dev = x.device
     if out is None:
-        out = torch.empty(x.shape[:-1] + (D // 2,), dtype=torch.uint8, device=x.device)
-    _check_dtype(out, (torch.uint8,), "out")
+        out = torch.empty(x.shape[:-1] + (dx.cols // 2,), dtype=torch.uint8, device=dev)
     if sb is None:
-        sb = (torch.empty(mma_scale_bytes(B, M, D // 16), dtype=torch.uint8, device=x.device) if mma else
-              torch.empty(x.shape[:-1] + (D // 16,), dtype=torch.float8_e4m3fn, device=x.device))
-    if mma:
-        _mma_scales(sb, B, M, D // 16, "sb")
-    elif sb.element_size() != 1 or not sb.is_contiguous() or sb.numel() != B * M * (D // 16):
-        raise ValueError("sb must be a contiguous one-byte tensor [.., M, D/16]")
+        sb = (torch.empty((n,), dtype=torch.uint8, device=dev) if mma else
+              torch.empty(x.shape[:-1] + (S,), dtype=torch.float8_e4m3fn, device=dev))
     if global_scale is None:
-        global_scale = torch.empty(B, dtype=torch.float32, device=x.device)
-    if global_scale.dtype != torch.float32 or not global_scale.is_contiguous() or global_scale.numel() != B:
-        raise ValueError("global_scale must be a contiguous float32 tensor of %d values" % B)
-    hh, dh = _norm_h(x, residual, h)
-    _same_device((x, out, sb, global_scale, hh))
-    dq = _desc(out, "out", packed=True)
-    with _on_device(x):
-        check(lib.rms_norm_nvfp4(ctypes.byref(dx), dr, weight.data_ptr(), eps, amax.data_ptr(), dh, ctypes.byref(dq),
-                                 sb.data_ptr(), int(mma), global_scale.data_ptr(), None, _stream(x)),
-              "rms_norm_nvfp4")
-    return out, sb, global_scale, hh
+        global_scale = torch.empty(B, dtype=torch.float32, device=dev)
+    _check_dtype(out, (torch.uint8,), "out")
+    _same_device(x, weight, residual, amax, out, sb, global_scale, h)
+    _launch(x, "rms_norm_nvfp4", px, pr, weight.data_ptr(), eps, _floats(amax, B, "amax"), ph,
+            ctypes.byref(_desc(out, "out", True)), _one_byte(sb, n, "sb", "tile" if mma else "dense"), int(mma),
+            _floats(global_scale, B, "global_scale"), None)
+    return out, sb, global_scale, h
 
 
 def rms_norm_fake_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -753,23 +747,19 @@ def rms_norm_fake_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optiona
         raise ValueError("format must be 'mxfp8' or 'nvfp4', got %r" % (format,))
     if (format == "nvfp4") != (amax is not None):
         raise ValueError("amax is given exactly with format='nvfp4'")
-    dx, dr, B = _norm_inputs(x, weight, residual, amax)
+    px, pr, ph, dx, h = _norm_inputs(x, weight, residual, h)
     if out is None:
         out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
     _check_dtype(out, (torch.bfloat16,), "out")
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    hh, dh = _norm_h(x, residual, h)
-    _same_device((x, out, hh))
-    dy = _desc(out, "out")
-    with _on_device(x):
-        if format == "mxfp8":
-            check(lib.rms_norm_mxfp8_fake_quant(ctypes.byref(dx), dr, weight.data_ptr(), eps, dh, ctypes.byref(dy),
-                                                rstd.data_ptr(), _stream(x)), "rms_norm_mxfp8_fake_quant")
-        else:
-            check(lib.rms_norm_nvfp4_fake_quant(ctypes.byref(dx), dr, weight.data_ptr(), eps, amax.data_ptr(), dh,
-                                                ctypes.byref(dy), rstd.data_ptr(), _stream(x)),
-                  "rms_norm_nvfp4_fake_quant")
-    return out, hh, rstd
+    _same_device(x, weight, residual, amax, out, h)
+    head = (px, pr, weight.data_ptr(), eps)
+    tail = (ph, ctypes.byref(_desc(out, "out")), rstd.data_ptr())
+    if format == "mxfp8":
+        _launch(x, "rms_norm_mxfp8_fake_quant", *head, *tail)
+    else:
+        _launch(x, "rms_norm_nvfp4_fake_quant", *head, _floats(amax, dx.batch, "amax"), *tail)
+    return out, h, rstd
 
 
 def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -781,29 +771,27 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
     dweight [D] is float32 or bfloat16, or None when not needed."""
     if dweight_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("dweight_dtype must be float32 or bfloat16")
-    for t, name in ((dy, "dy"), (h, "h")) + (((dh, "dh"),) if dh is not None else ()):
-        _check_dtype(t, (torch.bfloat16,), name)
-    _check_dtype(weight, (torch.bfloat16,), "weight")
-    if weight.dim() != 1 or weight.shape[0] != h.shape[-1] or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous 1-D tensor of %d values" % h.shape[-1])
-    if rstd.dtype != torch.float32 or not rstd.is_contiguous() or rstd.shape != h.shape[:-1]:
-        raise ValueError("rstd must be a contiguous float32 tensor %s" % (tuple(h.shape[:-1]),))
+    _check_dtype(dy, (torch.bfloat16,), "dy")
+    if dh is not None:
+        _check_dtype(dh, (torch.bfloat16,), "dh")
+    px, _, _, dhh, _ = _norm_inputs(h, weight, None, None)
+    if rstd.shape != h.shape[:-1]:
+        raise ValueError("rstd must have shape %s" % (tuple(h.shape[:-1]),))
     if out is None:
         out = torch.empty(h.shape, dtype=torch.bfloat16, device=h.device)
     _check_dtype(out, (torch.bfloat16,), "out")
-    _same_device((h, dy, weight, rstd, dh, out))
-    ddy, dhh, dx = _desc(dy, "dy"), _desc(h, "h"), _desc(out, "out")
-    ddh = ctypes.byref(_desc(dh, "dh")) if dh is not None else None
-    with _on_device(h):
-        dw = ws = None
-        if need_dweight:
-            dw = torch.empty(h.shape[-1], dtype=dweight_dtype, device=h.device)
-            n = int(lib.rms_norm_backward_workspace_size(ctypes.byref(dhh)))
-            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=h.device)
-        check(lib.rms_norm_backward(ctypes.byref(ddy), ddh, ctypes.byref(dhh), weight.data_ptr(), rstd.data_ptr(),
-                                    ctypes.byref(dx), dw.data_ptr() if need_dweight else None,
-                                    int(dweight_dtype == torch.bfloat16), ws.data_ptr() if need_dweight else None,
-                                    ws.numel() if need_dweight else 0, _stream(h)), "rms_norm_backward")
+    _same_device(h, dy, weight, rstd, dh, out)
+    dw, ws, n = None, None, 0
+    if need_dweight:
+        with torch.cuda.device(h.device):     # the size depends on the device
+            n = max(int(lib.rms_norm_backward_workspace_size(px)), 256)
+        dw = torch.empty(dhh.cols, dtype=dweight_dtype, device=h.device)
+        ws = torch.empty(n, dtype=torch.uint8, device=h.device)
+    _launch(h, "rms_norm_backward", ctypes.byref(_desc(dy, "dy")),
+            ctypes.byref(_desc(dh, "dh")) if dh is not None else None, px, weight.data_ptr(),
+            _floats(rstd, dhh.batch * dhh.rows, "rstd"), ctypes.byref(_desc(out, "out")),
+            dw.data_ptr() if need_dweight else None, int(dweight_dtype == torch.bfloat16),
+            ws.data_ptr() if need_dweight else None, n)
     return out, dw
 
 

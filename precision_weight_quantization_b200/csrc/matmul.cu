@@ -36,6 +36,14 @@ __device__ __forceinline__ bool wait_or_record(uint32_t bar, uint32_t parity) {
     return false;
 }
 
+// True in every thread of the epilogue's 128 when `ok` is true in all of them.
+__device__ __forceinline__ bool vote_all(bool ok) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)ok) : "memory");
+    return r != 0u;
+}
+
 // ga * gw as a product of two FP32 factors, so that neither the scale nor a
 // partial product leaves the FP32 range when the result does not: one factor
 // is 1 unless the product of the scales is outside [2^-100, 2^100].
@@ -229,6 +237,251 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
     if (warp == 5) tmem_free<1>(tmem, C::kCols);
 }
 
+// ---------------------------------------------------------------- many tokens: CTA pairs
+//
+// A pair of CTAs (two SMs, cta_group::2) takes 256 weight rows, 128 per CTA,
+// times up to 256 tokens, half of whose codes each CTA loads: per 128-byte
+// step of K an SM brings in 32 KB of codes for 512 tensor-core clocks, half
+// of what one CTA alone would need for a 128 x 256 tile.  The kernel is
+// persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
+// that the pairs at work share operands in L2.
+//
+// Tensor memory: 512 columns hold two scale buffers (a step's scales are
+// copied while the previous step's are read) and two accumulators that
+// overlap where two of 256 columns do not fit: the epilogue empties the
+// shared columns first and then lets the next tile begin, while it writes
+// the rest.
+//
+// The token tile is a multiple of 64 columns up to 256, or of 32 when one
+// tile holds every token: the MMA takes scale columns two by two, so a tile
+// starts at a multiple of 64 rows of a 128-row band (and its scales span at
+// most two bands).  The host picks the one with the least work in the last wave.
+//
+// Warps 0..3 epilogue, 4 TMA producer, 5 MMA issuer (first CTA) and TMEM owner.
+
+constexpr int kPairThreads = 192;
+constexpr uint32_t kGroup = 8;
+constexpr int kOutTokens = 32;                                    // tokens per output store
+constexpr uint32_t kOutBytes = 128u * kOutTokens * 2u;            // 128 weight rows x 32 tokens, BF16
+
+struct PairArgs {
+    CUtensorMap w, ws, t, ts, y;
+    const float* gt;
+    const float* gw;
+    uint16_t* yp;                // y_tma == 0: element stores
+    int64_t y_bs, y_rs;          // elements
+    int y_tma;
+    int n, m;
+    int w_bands, t_bands;
+    int steps, last_mmas;
+    int tile_t, t_band_box;      // tokens per tile, scale bands per tile
+    uint32_t w_tiles, t_tiles, tiles;
+    FastDiv per_batch, per_group;   // w_tiles * t_tiles, w_tiles * kGroup
+};
+
+template <ProductFormat kF>
+struct PairCfg {
+    using T = ProductTraits<kF>;
+    static constexpr uint32_t kW = 128u * kStepBytes, kT = 128u * kStepBytes;
+    static constexpr uint32_t kStage = kW + kT + (T::kFp4 ? 6144u : 2048u);   // scales: one band of weights, two of tokens
+    static constexpr int kStages = T::kFp4 ? 5 : 6;
+    static constexpr uint32_t kSmem = kStages * kStage + 2u * kOutBytes + 1024u;
+    static constexpr uint32_t kScaleCols = 12u * T::kScaleTiles;              // per buffer: 4 weights + 8 tokens per tile
+    static constexpr uint32_t kScaleAt = 512u - 2u * kScaleCols;
+    static constexpr uint32_t kAcc1 = T::kFp4 ? 160u : 224u;                  // second accumulator
+    static_assert(kAcc1 + 256u <= kScaleAt, "TMEM");
+    static_assert(3u * T::kScaleBytes <= kStage - kW - kT && kStage % 1024u == 0, "stage");
+    static_assert(kSmem <= 232448u, "shared memory");
+};
+
+struct PairTile {
+    int wt, tt, b;
+};
+__device__ __forceinline__ PairTile pair_tile(const PairArgs& a, uint32_t i) {
+    PairTile r;
+    const uint32_t b = fdiv(i, a.per_batch);
+    i -= b * a.per_batch.d;
+    const uint32_t g = fdiv(i, a.per_group);
+    i -= g * a.per_group.d;
+    const uint32_t in_group = min(kGroup, a.t_tiles - g * kGroup);
+    r.wt = (int)(i / in_group);
+    r.tt = (int)(g * kGroup + i - (uint32_t)r.wt * in_group);
+    r.b = (int)b;
+    return r;
+}
+
+template <ProductFormat kF>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_kernel(const __grid_constant__ PairArgs a) {
+    using T = ProductTraits<kF>;
+    using C = PairCfg<kF>;
+    constexpr int kS = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kS + 4];
+    __shared__ uint32_t tmem_word;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, stage_out = ring + kS * C::kStage;
+    const uint32_t full = smem_addr(bars), empty = full + 8u * kS;
+    const uint32_t acc_full = empty + 8u * kS, acc_free = acc_full + 16u;   // [2] each
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    // accumulator columns that the two buffers share
+    const int shared_cols = max(0, a.tile_t - (int)C::kAcc1);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kS; ++i) {
+            mbar_init(full + 8u * i, 1);
+            mbar_init(empty + 8u * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8u * i, 1);
+            mbar_init(acc_free + 8u * i, 8);   // four epilogue warps of either CTA
+        }
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc<2>(smem_addr(&tmem_word), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_word;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            const uint32_t tok_bytes = (uint32_t)a.tile_t / 2u * kStepBytes;
+            const uint32_t bytes = C::kW + tok_bytes + (1u + (uint32_t)a.t_band_box) * T::kScaleBytes;
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t i = first; ok && i < a.tiles; i += stride) {
+                const PairTile p = pair_tile(a, i);
+                const int wt = p.wt * 2 + (int)rank, t0 = p.tt * a.tile_t;
+                for (int s = 0; s < a.steps; ++s, ++it) {
+                    const uint32_t st = it % kS;
+                    if (it >= kS && !wait_or_record(empty + 8u * st, (it / kS - 1u) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = ring + st * C::kStage, bar = cluster_addr(full + 8u * st, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8u * st, 2u * bytes);
+                    tma_load_3d_pair(at, &a.w, bar, s * (int)kStepBytes, wt * 128, p.b);
+                    tma_load_3d_pair(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0 + (int)rank * (a.tile_t / 2), p.b);
+                    tma_load_3d_pair(at + C::kW + C::kT, &a.ws, bar, 0, s * T::kScaleTiles,
+                                     p.b * a.w_bands + wt);
+                    tma_load_3d_pair(at + C::kW + C::kT + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
+                                     p.b * a.t_bands + t0 / 128);
+                }
+            }
+            // no copy of either CTA is in flight when the pair ends
+            if (rank == 0)
+                for (uint32_t j = it > kS ? it - kS : 0u; j < it; ++j) wait_or_record(full + 8u * (j % kS), (j / kS) & 1u);
+        }
+    } else if (warp == 5) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = mma_idesc<kF>(256, a.tile_t);
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (uint32_t i = first; ok && i < a.tiles; i += stride, ++n) {
+                const PairTile p = pair_tile(a, i);
+                const uint32_t buf = n & 1u, acc = tmem + buf * C::kAcc1;
+                const uint32_t tok_col = (uint32_t)(p.tt * a.tile_t % 128) / 32u;
+                // the accumulator is free: with shared columns, once the previous tile's have been read;
+                // without, once the tile before that has been read
+                if (shared_cols > 0 && n >= 1) ok = wait_or_record(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
+                if (shared_cols == 0 && n >= 2) ok = wait_or_record(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
+                if (!ok) break;
+                fence_cluster();
+                tc_fence_after();
+                for (int s = 0; s < a.steps; ++s, ++it) {
+                    const uint32_t st = it % kS;
+                    if (!wait_or_record(full + 8u * st, (it / kS) & 1u) ||
+                        // the scale columns of two steps ago are read no more
+                        (it >= 2 && !wait_or_record(empty + 8u * ((it - 2u) % kS), ((it - 2u) / kS) & 1u))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = ring + st * C::kStage, sc = at + C::kW + C::kT;
+                    const uint32_t sw = tmem + C::kScaleAt + (it & 1u) * C::kScaleCols, sx = sw + 4u * T::kScaleTiles;
+#pragma unroll
+                    for (int j = 0; j < T::kScaleTiles; ++j) {
+                        copy_scales<2>(sw + 4u * j, desc_scales(sc + 512u * j));
+                        copy_scales<2>(sx + 8u * j, desc_scales(sc + T::kScaleBytes + 512u * j));
+                        if (a.t_band_box == 2)
+                            copy_scales<2>(sx + 8u * j + 4u, desc_scales(sc + 2u * T::kScaleBytes + 512u * j));
+                    }
+                    const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
+                    const int mmas = s == a.steps - 1 ? a.last_mmas : kMmasPerStep;
+                    for (int j = 0; j < mmas; ++j) {
+                        const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
+                        mma_block_scaled<kF, 2>(acc, dw + 2u * j, dx + 2u * j, id, sw + (T::kFp4 ? 4u * j : 0u),
+                                                sx + (T::kFp4 ? 8u * j : 0u) + tok_col, (s | j) != 0);
+                    }
+                    mma_commit_pair(empty + 8u * st);
+                }
+                mma_commit_pair(acc_full + 8u * buf);
+            }
+        }
+    } else {
+        uint32_t n = 0, stores = 0;
+        const uint32_t row = tmem + ((uint32_t)warp << 21);
+        for (uint32_t i = first; i < a.tiles; i += stride, ++n) {
+            const PairTile p = pair_tile(a, i);
+            const uint32_t buf = n & 1u, acc = row + buf * C::kAcc1, free_bar = cluster_addr(acc_free + 8u * buf, 0);
+            const int n0 = (p.wt * 2 + (int)rank) * 128, t0 = p.tt * a.tile_t, chunks = a.tile_t / 32;
+            const float2 sc = output_scale(a.gt, a.gw, p.b);
+            if (!vote_all(wait_or_record(acc_full + 8u * buf, (n / 2u) & 1u))) break;   // the four warps leave together
+            tc_fence_after();
+            const int nn = n0 + warp * 32 + lane;
+            uint16_t* yp = a.yp + (int64_t)p.b * a.y_bs + nn;
+            for (int k = 0; k < chunks; ++k) {
+                // shared columns first: the first buffer's last ones, the second buffer's first ones
+                const int c0 = 32 * (buf == 0 ? chunks - 1 - k : k);
+                uint32_t v[32];
+                tmem_ld32(acc + c0, v);
+                tmem_ld_wait();
+                if (32 * (k + 1) == max(32 * chunks * (shared_cols == 0), shared_cols)) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(free_bar);
+                }
+                const int t = t0 + c0;
+                if (t >= a.m || n0 >= a.n) continue;   // the same for the CTA
+                if (a.y_tma) {
+                    // the staging buffer of two stores ago has been read
+                    const uint32_t out = stage_out + (stores & 1u) * kOutBytes;
+                    ++stores;
+                    if (threadIdx.x == 0) bulk_wait_read<1>();
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    const uint32_t dst = out + threadIdx.x * 2u;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const uint32_t two = pack_bf16x2(__uint_as_float(v[c]) * sc.x * sc.y,
+                                                         __uint_as_float(v[c + 1]) * sc.x * sc.y);
+                        asm volatile("st.shared.b16 [%0], %1;" :: "r"(dst + c * 256u), "h"((uint16_t)two) : "memory");
+                        asm volatile("st.shared.b16 [%0], %1;" :: "r"(dst + c * 256u + 256u), "h"((uint16_t)(two >> 16))
+                                     : "memory");
+                    }
+                    fence_async_shared();
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (threadIdx.x == 0) {
+                        tma_store_3d(&a.y, out, n0, t, p.b);
+                        bulk_commit();
+                    }
+                } else if (nn < a.n) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (t + c < a.m) yp[(int64_t)(t + c) * a.y_rs] = bf16_bits(__uint_as_float(v[c]) * sc.x * sc.y);
+                }
+            }
+        }
+        if (threadIdx.x == 0) bulk_wait<0>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs are done with TMEM, barriers and operands
+    if (warp == 5) tmem_free<2>(tmem, 512);
+}
+
 // ---------------------------------------------------------------- host side
 
 // Code rows [batch][rows][bytes] as a 3-D map of 128-byte wide boxes, 128-byte swizzle.
@@ -304,10 +557,85 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Tokens per tile of the pair kernel: the least (waves of tiles) x (columns
+// of a tile + a fixed cost in columns).  kTileCost is the measured cost of a
+// tile's start and of its weight operand.
+constexpr int kTileCost = 48;
+int pair_tile_tokens(int64_t m, int64_t w_tiles, int64_t batch, int64_t pairs) {
+    int best = 256;
+    int64_t best_cost = -1;
+    for (int t = 256; t >= 32; t -= 32) {
+        if (t % 64 != 0 && m > t) continue;
+        const int64_t tiles = batch * w_tiles * ((m + t - 1) / t);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (t + kTileCost);
+        if (best_cost < 0 || cost < best_cost) {
+            best = t;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+template <ProductFormat kF>
+cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s) {
+    using T = ProductTraits<kF>;
+    using C = PairCfg<kF>;
+    static int configured[kMaxDevices] = {0};
+    const void* fn = (const void*)pair_kernel<kF>;
+    cudaError_t e = set_smem_limit_once(configured, &fn, 1, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t row_bytes = T::kFp4 ? p.k / 2 : p.k;
+    const int64_t col_tiles = mma_scale_col_tiles(p.k / (T::kFp4 ? 16 : 32));
+    const int64_t pairs = sm_count(current_device()) / 2, w_tiles = (p.w.rows + 255) / 256;
+    PairArgs a;
+    a.tile_t = pair_tile_tokens(p.a.rows, w_tiles, p.a.batch, pairs);
+    a.t_band_box = 128 % a.tile_t == 0 ? 1 : 2;
+    const int64_t t_tiles = (p.a.rows + a.tile_t - 1) / a.tile_t;
+    a.w_bands = (int)((p.w.rows + 127) / 128);
+    a.t_bands = (int)((p.a.rows + 127) / 128);
+    if (!code_map(encode, &a.w, p.w, row_bytes, 128) ||
+        !code_map(encode, &a.t, p.a, row_bytes, (uint32_t)a.tile_t / 2) ||
+        !scale_map(encode, &a.ws, p.w_scale, p.a.batch * a.w_bands, col_tiles, T::kScaleTiles, 1) ||
+        !scale_map(encode, &a.ts, p.a_scale, p.a.batch * a.t_bands, col_tiles, T::kScaleTiles,
+                   (uint32_t)a.t_band_box))
+        return cudaErrorInvalidValue;
+    // output by TMA where its rows are whole 16-byte units at 16-byte addresses (a store that ends inside a
+    // unit overwrites the rest of it), else element by element
+    a.y_tma = p.y.cols % 8 == 0 && (uintptr_t)p.y.ptr % 16 == 0 && p.y.rstride % 16 == 0 && (p.y.batch == 1 || p.y.bstride % 16 == 0);
+    if (a.y_tma) {
+        const cuuint64_t dims[3] = {(cuuint64_t)p.y.cols, (cuuint64_t)p.y.rows, (cuuint64_t)p.y.batch};
+        const cuuint64_t strides[2] = {(cuuint64_t)p.y.rstride,
+                                       (cuuint64_t)(p.y.batch > 1 ? p.y.bstride : p.y.rows * p.y.rstride)};
+        const cuuint32_t box[3] = {128, kOutTokens, 1}, es[3] = {1, 1, 1};
+        if (encode(&a.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.y.ptr, dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    a.gt = p.a_gs;
+    a.gw = p.w_gs;
+    a.yp = reinterpret_cast<uint16_t*>(p.y.ptr);
+    a.y_bs = p.y.bstride / 2;
+    a.y_rs = p.y.rstride / 2;
+    a.n = (int)p.w.rows;
+    a.m = (int)p.a.rows;
+    a.steps = (int)((row_bytes + kStepBytes - 1) / kStepBytes);
+    a.last_mmas = (int)((row_bytes - (int64_t)(a.steps - 1) * kStepBytes + 31) / 32);
+    a.w_tiles = (uint32_t)w_tiles;
+    a.t_tiles = (uint32_t)t_tiles;
+    a.tiles = (uint32_t)(p.a.batch * w_tiles * t_tiles);
+    a.per_batch = make_fastdiv((uint32_t)(w_tiles * t_tiles));
+    a.per_group = make_fastdiv((uint32_t)w_tiles * kGroup);
+    const unsigned grid = 2u * (unsigned)std::min<int64_t>(a.tiles, pairs);
+    pair_kernel<kF><<<grid, kPairThreads, C::kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <ProductFormat kF>
 cudaError_t launch_product(const Product& p, cudaStream_t s) {
     EncodeTiledFn encode = encode_tiled_fn();
     if (!encode) return cudaErrorNotSupported;
+    if (p.a.rows > 64) return launch_pairs<kF>(p, encode, s);
     // tokens per tile: the smallest MMA width that holds them all, at most 128
     if (p.a.rows <= 16) return launch_tokens<kF, 16>(p, encode, s);
     if (p.a.rows <= 32) return launch_tokens<kF, 32>(p, encode, s);
