@@ -36,6 +36,11 @@ __device__ __forceinline__ bool wait_or_record(uint32_t bar, uint32_t parity) {
     return false;
 }
 
+// The same for a converged warp: every lane waits, and all get one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_record(bar, parity));
+}
+
 // True in every thread of the epilogue's 128 when `ok` is true in all of them.
 __device__ __forceinline__ bool vote_all(bool ok) {
     uint32_t r;
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
     __shared__ uint32_t tmem_word;
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t full = smem_addr(bars), empty = full + 8u * kS, done = full + 16u * kS;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     const uint32_t rank = blockIdx.x % (uint32_t)a.split;
     uint32_t tile = blockIdx.x / (uint32_t)a.split;
@@ -135,53 +140,58 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_word;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_word, 0);
 
     if (warp == 4) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < steps; ++i) {
-                const int st = i % kS;
-                if (i >= kS && !wait_or_record(empty + 8u * st, ((i / kS) - 1) & 1)) break;
-                const uint32_t at = ring + (uint32_t)st * C::kStage, bar = full + 8u * st;
+        int i = 0;
+        for (; i < steps; ++i) {
+            const int st = i % kS;
+            if (i >= kS && !warp_wait(empty + 8u * st, ((i / kS) - 1) & 1)) break;
+            const uint32_t at = ring + (uint32_t)st * C::kStage, bar = full + 8u * st;
+            const int s = s0 + i;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(bar, C::kStage);
-                const int s = s0 + i;
                 tma_load_3d(at, &a.w, bar, s * (int)kStepBytes, n0, b);
                 tma_load_3d(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0, b);
                 tma_load_3d(at + C::kW + C::kT, &a.ws, bar, 0, s * T::kScaleTiles, b * a.w_bands + wt);
                 tma_load_3d(at + C::kW + C::kT + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
                             b * a.t_bands + t0 / 128);
             }
-            // no copy is in flight when the CTA ends
-            for (int j = max(0, i - kS); j < i; ++j) wait_or_record(full + 8u * (j % kS), (j / kS) & 1);
+            __syncwarp();
         }
+        // no copy is in flight when the CTA ends
+        for (int j = max(0, i - kS); j < i; ++j) warp_wait(full + 8u * (j % kS), (j / kS) & 1);
     } else if (warp == 5) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = mma_idesc<kF>(128, kTok);
-            for (int i = 0; i < steps; ++i) {
-                const int st = i % kS;
-                if (!wait_or_record(full + 8u * st, (i / kS) & 1)) break;
-                // the scale columns of step i - 2 are read no more
-                if (i >= 2 && !wait_or_record(empty + 8u * ((i - 2) % kS), ((i - 2) / kS) & 1)) break;
-                tc_fence_after();
-                const uint32_t at = ring + (uint32_t)st * C::kStage;
-                const uint32_t sw = tmem + kTok + (uint32_t)(i & 1) * 2u * C::kScaleCols, sx = sw + C::kScaleCols;
+        constexpr uint32_t idesc = mma_idesc<kF>(128, kTok);
+        for (int i = 0; i < steps; ++i) {
+            const int st = i % kS;
+            if (!warp_wait(full + 8u * st, (i / kS) & 1)) break;
+            // the scale columns of step i - 2 are read no more
+            if (i >= 2 && !warp_wait(empty + 8u * ((i - 2) % kS), ((i - 2) / kS) & 1)) break;
+            tc_fence_after();
+            const uint32_t at = ring + (uint32_t)st * C::kStage;
+            const uint32_t sw = tmem + kTok + (uint32_t)(i & 1) * 2u * C::kScaleCols, sx = sw + C::kScaleCols;
+            const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
+            const int mmas = s0 + i == a.steps - 1 ? a.last_mmas : kMmasPerStep;
+            if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < T::kScaleTiles; ++j) {
                     copy_scales<1>(sw + 4u * j, desc_scales(at + C::kW + C::kT + 512u * j));
                     copy_scales<1>(sx + 4u * j, desc_scales(at + C::kW + C::kT + T::kScaleBytes + 512u * j));
                 }
-                const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
-                const int mmas = s0 + i == a.steps - 1 ? a.last_mmas : kMmasPerStep;
-                for (int j = 0; j < mmas; ++j) {
+#pragma unroll
+                for (int j = 0; j < kMmasPerStep; ++j) {
+                    if (j >= mmas) break;
                     const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
                     const uint32_t so = T::kFp4 ? 4u * j : 0u;
                     mma_block_scaled<kF, 1>(tmem, dw + 2u * j, dx + 2u * j, id, sw + so, sx + so, (i | j) != 0);
                 }
                 mma_commit(empty + 8u * st);
             }
-            mma_commit(done);
+            __syncwarp();
         }
+        if (elect_one()) mma_commit(done);
+        __syncwarp();
     } else {
         const bool ok = wait_or_record(done, 0);
         tc_fence_after();
@@ -322,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, stage_out = ring + kS * C::kStage;
     const uint32_t full = smem_addr(bars), empty = full + 8u * kS;
     const uint32_t acc_full = empty + 8u * kS, acc_free = acc_full + 16u;   // [2] each
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     // accumulator columns that the two buffers share
@@ -344,24 +354,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = tmem_word;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_word, 0);
 
     if (warp == 4) {
-        if (lane == 0) {
-            const uint32_t tok_bytes = (uint32_t)a.tile_t / 2u * kStepBytes;
-            const uint32_t bytes = C::kW + tok_bytes + (1u + (uint32_t)a.t_band_box) * T::kScaleBytes;
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t i = first; ok && i < a.tiles; i += stride) {
-                const PairTile p = pair_tile(a, i);
-                const int wt = p.wt * 2 + (int)rank, t0 = p.tt * a.tile_t;
-                for (int s = 0; s < a.steps; ++s, ++it) {
-                    const uint32_t st = it % kS;
-                    if (it >= kS && !wait_or_record(empty + 8u * st, (it / kS - 1u) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t at = ring + st * C::kStage, bar = cluster_addr(full + 8u * st, 0);
+        const uint32_t tok_bytes = (uint32_t)a.tile_t / 2u * kStepBytes;
+        const uint32_t bytes = C::kW + tok_bytes + (1u + (uint32_t)a.t_band_box) * T::kScaleBytes;
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t i = first; ok && i < a.tiles; i += stride) {
+            const PairTile p = pair_tile(a, i);
+            const int wt = p.wt * 2 + (int)rank, t0 = p.tt * a.tile_t;
+            for (int s = 0; s < a.steps; ++s, ++it) {
+                const uint32_t st = it % kS;
+                if (it >= kS && !warp_wait(empty + 8u * st, (it / kS - 1u) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = ring + st * C::kStage, bar = cluster_addr(full + 8u * st, 0);
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full + 8u * st, 2u * bytes);
                     tma_load_3d_pair(at, &a.w, bar, s * (int)kStepBytes, wt * 128, p.b);
                     tma_load_3d_pair(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0 + (int)rank * (a.tile_t / 2), p.b);
@@ -370,13 +380,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tma_load_3d_pair(at + C::kW + C::kT + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
                                      p.b * a.t_bands + t0 / 128);
                 }
+                __syncwarp();
             }
-            // no copy of either CTA is in flight when the pair ends
-            if (rank == 0)
-                for (uint32_t j = it > kS ? it - kS : 0u; j < it; ++j) wait_or_record(full + 8u * (j % kS), (j / kS) & 1u);
         }
+        // no copy of either CTA is in flight when the pair ends
+        if (rank == 0)
+            for (uint32_t j = it > kS ? it - kS : 0u; j < it; ++j) warp_wait(full + 8u * (j % kS), (j / kS) & 1u);
     } else if (warp == 5) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             const uint32_t idesc = mma_idesc<kF>(256, a.tile_t);
             uint32_t it = 0, n = 0;
             bool ok = true;
@@ -386,39 +397,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t tok_col = (uint32_t)(p.tt * a.tile_t % 128) / 32u;
                 // the accumulator is free: with shared columns, once the previous tile's have been read;
                 // without, once the tile before that has been read
-                if (shared_cols > 0 && n >= 1) ok = wait_or_record(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
-                if (shared_cols == 0 && n >= 2) ok = wait_or_record(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
+                if (shared_cols > 0 && n >= 1) ok = warp_wait(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
+                if (shared_cols == 0 && n >= 2) ok = warp_wait(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
                 if (!ok) break;
                 fence_cluster();
                 tc_fence_after();
                 for (int s = 0; s < a.steps; ++s, ++it) {
                     const uint32_t st = it % kS;
-                    if (!wait_or_record(full + 8u * st, (it / kS) & 1u) ||
+                    if (!warp_wait(full + 8u * st, (it / kS) & 1u) ||
                         // the scale columns of two steps ago are read no more
-                        (it >= 2 && !wait_or_record(empty + 8u * ((it - 2u) % kS), ((it - 2u) / kS) & 1u))) {
+                        (it >= 2 && !warp_wait(empty + 8u * ((it - 2u) % kS), ((it - 2u) / kS) & 1u))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t at = ring + st * C::kStage, sc = at + C::kW + C::kT;
                     const uint32_t sw = tmem + C::kScaleAt + (it & 1u) * C::kScaleCols, sx = sw + 4u * T::kScaleTiles;
-#pragma unroll
-                    for (int j = 0; j < T::kScaleTiles; ++j) {
-                        copy_scales<2>(sw + 4u * j, desc_scales(sc + 512u * j));
-                        copy_scales<2>(sx + 8u * j, desc_scales(sc + T::kScaleBytes + 512u * j));
-                        if (a.t_band_box == 2)
-                            copy_scales<2>(sx + 8u * j + 4u, desc_scales(sc + 2u * T::kScaleBytes + 512u * j));
-                    }
                     const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
                     const int mmas = s == a.steps - 1 ? a.last_mmas : kMmasPerStep;
-                    for (int j = 0; j < mmas; ++j) {
-                        const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
-                        mma_block_scaled<kF, 2>(acc, dw + 2u * j, dx + 2u * j, id, sw + (T::kFp4 ? 4u * j : 0u),
-                                                sx + (T::kFp4 ? 8u * j : 0u) + tok_col, (s | j) != 0);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < T::kScaleTiles; ++j) {
+                            copy_scales<2>(sw + 4u * j, desc_scales(sc + 512u * j));
+                            copy_scales<2>(sx + 8u * j, desc_scales(sc + T::kScaleBytes + 512u * j));
+                            if (a.t_band_box == 2)
+                                copy_scales<2>(sx + 8u * j + 4u, desc_scales(sc + 2u * T::kScaleBytes + 512u * j));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kMmasPerStep; ++j) {
+                            if (j >= mmas) break;
+                            const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
+                            mma_block_scaled<kF, 2>(acc, dw + 2u * j, dx + 2u * j, id, sw + (T::kFp4 ? 4u * j : 0u),
+                                                    sx + (T::kFp4 ? 8u * j : 0u) + tok_col, (s | j) != 0);
+                        }
+                        mma_commit_pair(empty + 8u * st);
                     }
-                    mma_commit_pair(empty + 8u * st);
+                    __syncwarp();
                 }
-                mma_commit_pair(acc_full + 8u * buf);
+                if (elect_one()) mma_commit_pair(acc_full + 8u * buf);
+                __syncwarp();
             }
         }
     } else {

@@ -55,6 +55,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// ---------------------------------------------------------------- warp-uniform roles
+//
+// TMA and tcgen05 instructions take their operands from uniform registers.
+// A producer or issuer loop that runs in one lane of a diverged warp pays
+// about 65 to 130 clocks per instruction to bring them there (measured: an
+// MMA step of 12 scale copies and 4 MMAs issued in 1800 clocks); the same
+// loop run by the whole converged warp, with one elected lane at the
+// instructions, issues them back to back.
+
+// The warp's index as a value that the compiler knows to be uniform.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
+}
+
 // ---------------------------------------------------------------- descriptors
 
 // K-major operand tile in shared memory, rows of 128 bytes in the 128-byte
