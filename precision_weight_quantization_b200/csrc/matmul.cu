@@ -256,11 +256,15 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
 // that the pairs at work share operands in L2.
 //
-// Tensor memory: 512 columns hold two scale buffers (a step's scales are
-// copied while the previous step's are read) and two accumulators that
-// overlap where two of 256 columns do not fit: the epilogue empties the
-// shared columns first and then lets the next tile begin, while it writes
-// the rest.
+// Tensor memory: 512 columns hold three scale buffers (a step's scales are
+// copied once the MMAs of the step three before have been seen to end; with
+// two buffers that wait cost 10 to 13 % of the step) and two accumulators
+// that overlap where two of 256 columns do not fit: the epilogue takes the
+// shared columns into registers first and then lets the next tile begin.
+//
+// Output: 32 tokens at a time, TMEM fragments are transposed by stmatrix into
+// [token][64 weight rows] boxes (128-byte swizzle, no bank conflicts) and
+// stored by TMA, one warp pair per box.
 //
 // The token tile is a multiple of 64 columns up to 256, or of 32 when one
 // tile holds every token: the MMA takes scale columns two by two, so a tile
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 constexpr int kPairThreads = 192;
 constexpr uint32_t kGroup = 8;
 constexpr int kOutTokens = 32;                                    // tokens per output store
-constexpr uint32_t kOutBytes = 128u * kOutTokens * 2u;            // 128 weight rows x 32 tokens, BF16
+constexpr uint32_t kOutBytes = 64u * kOutTokens * 2u;             // 64 weight rows x 32 tokens, BF16
 
 struct PairArgs {
     CUtensorMap w, ws, t, ts, y;
@@ -293,15 +297,18 @@ template <ProductFormat kF>
 struct PairCfg {
     using T = ProductTraits<kF>;
     static constexpr uint32_t kW = 128u * kStepBytes, kT = 128u * kStepBytes;
-    static constexpr uint32_t kStage = kW + kT + (T::kFp4 ? 6144u : 2048u);   // scales: one band of weights, two of tokens
+    static constexpr uint32_t kStage = kW + kT;                               // codes
+    static constexpr uint32_t kScales = 3u * T::kScaleBytes;                  // one band of weights, two of tokens
     static constexpr int kStages = T::kFp4 ? 5 : 6;
-    static constexpr uint32_t kSmem = kStages * kStage + 2u * kOutBytes + 1024u;
+    static constexpr uint32_t kOutBufs = T::kFp4 ? 4u : 3u;                   // output staging buffers per warp pair
+    static constexpr uint32_t kOutAt = kStages * kStage, kScalesAt = kOutAt + 2u * kOutBufs * kOutBytes;
+    static constexpr uint32_t kSmem = kScalesAt + kStages * kScales + 1024u;
+    static constexpr uint32_t kScaleBufs = 3u;
     static constexpr uint32_t kScaleCols = 12u * T::kScaleTiles;              // per buffer: 4 weights + 8 tokens per tile
-    static constexpr uint32_t kScaleAt = 512u - 2u * kScaleCols;
-    static constexpr uint32_t kAcc1 = T::kFp4 ? 160u : 224u;                  // second accumulator
-    static_assert(kAcc1 + 256u <= kScaleAt, "TMEM");
-    static_assert(3u * T::kScaleBytes <= kStage - kW - kT && kStage % 1024u == 0, "stage");
-    static_assert(kSmem <= 232448u, "shared memory");
+    static constexpr uint32_t kScaleAt = 512u - kScaleBufs * kScaleCols;
+    static constexpr uint32_t kAcc1 = (kScaleAt - 256u) / 32u * 32u;          // second accumulator
+    static constexpr int kMaxShared = (256 - (int)kAcc1) / 32;                // 32-column chunks in both
+    static_assert(kSmem <= 232448u - 256u, "shared memory");
 };
 
 struct PairTile {
@@ -329,14 +336,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * kS + 4];
     __shared__ uint32_t tmem_word;
-    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, stage_out = ring + kS * C::kStage;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, scales = ring + C::kScalesAt;
     const uint32_t full = smem_addr(bars), empty = full + 8u * kS;
     const uint32_t acc_full = empty + 8u * kS, acc_free = acc_full + 16u;   // [2] each
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-    // accumulator columns that the two buffers share
-    const int shared_cols = max(0, a.tile_t - (int)C::kAcc1);
+    // 32-column chunks that the two accumulators share
+    const int shared = max(0, a.tile_t - (int)C::kAcc1) / 32;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kS; ++i) {
@@ -375,9 +382,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (rank == 0) mbar_arrive_expect_tx(full + 8u * st, 2u * bytes);
                     tma_load_3d_pair(at, &a.w, bar, s * (int)kStepBytes, wt * 128, p.b);
                     tma_load_3d_pair(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0 + (int)rank * (a.tile_t / 2), p.b);
-                    tma_load_3d_pair(at + C::kW + C::kT, &a.ws, bar, 0, s * T::kScaleTiles,
-                                     p.b * a.w_bands + wt);
-                    tma_load_3d_pair(at + C::kW + C::kT + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
+                    const uint32_t sc = scales + st * C::kScales;
+                    tma_load_3d_pair(sc, &a.ws, bar, 0, s * T::kScaleTiles, p.b * a.w_bands + wt);
+                    tma_load_3d_pair(sc + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
                                      p.b * a.t_bands + t0 / 128);
                 }
                 __syncwarp();
@@ -397,22 +404,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t tok_col = (uint32_t)(p.tt * a.tile_t % 128) / 32u;
                 // the accumulator is free: with shared columns, once the previous tile's have been read;
                 // without, once the tile before that has been read
-                if (shared_cols > 0 && n >= 1) ok = warp_wait(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
-                if (shared_cols == 0 && n >= 2) ok = warp_wait(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
+                if (shared > 0 && n >= 1) ok = warp_wait(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
+                if (shared == 0 && n >= 2) ok = warp_wait(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
                 if (!ok) break;
                 fence_cluster();
                 tc_fence_after();
                 for (int s = 0; s < a.steps; ++s, ++it) {
                     const uint32_t st = it % kS;
                     if (!warp_wait(full + 8u * st, (it / kS) & 1u) ||
-                        // the scale columns of two steps ago are read no more
-                        (it >= 2 && !warp_wait(empty + 8u * ((it - 2u) % kS), ((it - 2u) / kS) & 1u))) {
+                        // the buffer's last scales are read no more
+                        (it >= C::kScaleBufs && !warp_wait(empty + 8u * ((it - C::kScaleBufs) % kS),
+                                                           ((it - C::kScaleBufs) / kS) & 1u))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = ring + st * C::kStage, sc = at + C::kW + C::kT;
-                    const uint32_t sw = tmem + C::kScaleAt + (it & 1u) * C::kScaleCols, sx = sw + 4u * T::kScaleTiles;
+                    const uint32_t at = ring + st * C::kStage, sc = scales + st * C::kScales;
+                    const uint32_t sw = tmem + C::kScaleAt + it % C::kScaleBufs * C::kScaleCols;
+                    const uint32_t sx = sw + 4u * T::kScaleTiles;
                     const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
                     const int mmas = s == a.steps - 1 ? a.last_mmas : kMmasPerStep;
                     if (elect_one()) {
@@ -441,47 +450,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else {
         uint32_t n = 0, stores = 0;
         const uint32_t row = tmem + ((uint32_t)warp << 21);
+        const bool issuer = (warp & 1) == 0 && lane == 0;
+        const uint32_t out = ring + C::kOutAt + (uint32_t)(warp >> 1) * C::kOutBufs * kOutBytes;
+        // this lane's stmatrix row: token lane % 8 of eight, weight rows 8 (lane / 8) .. + 7 of the warp's 32
+        const uint32_t c8 = (uint32_t)lane & 7u;
+        const uint32_t frag = c8 * 128u + (((uint32_t)(warp & 1) * 4u + ((uint32_t)lane >> 3)) ^ c8) * 16u;
         for (uint32_t i = first; i < a.tiles; i += stride, ++n) {
             const PairTile p = pair_tile(a, i);
             const uint32_t buf = n & 1u, acc = row + buf * C::kAcc1, free_bar = cluster_addr(acc_free + 8u * buf, 0);
             const int n0 = (p.wt * 2 + (int)rank) * 128, t0 = p.tt * a.tile_t, chunks = a.tile_t / 32;
             const float2 sc = output_scale(a.gt, a.gw, p.b);
-            if (!vote_all(wait_or_record(acc_full + 8u * buf, (n / 2u) & 1u))) break;   // the four warps leave together
-            tc_fence_after();
             const int nn = n0 + warp * 32 + lane;
             uint16_t* yp = a.yp + (int64_t)p.b * a.y_bs + nn;
-            for (int k = 0; k < chunks; ++k) {
-                // shared columns first: the first buffer's last ones, the second buffer's first ones
-                const int c0 = 32 * (buf == 0 ? chunks - 1 - k : k);
-                uint32_t v[32];
-                tmem_ld32(acc + c0, v);
-                tmem_ld_wait();
-                if (32 * (k + 1) == max(32 * chunks * (shared_cols == 0), shared_cols)) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(free_bar);
-                }
-                const int t = t0 + c0;
-                if (t >= a.m || n0 >= a.n) continue;   // the same for the CTA
+            // shared columns first: the first buffer's last ones, the second buffer's first ones
+            auto column = [&](int k) { return 32 * (buf == 0 ? chunks - 1 - k : k); };
+            auto load = [&](int k, uint32_t (&v)[32]) {
                 if (a.y_tma) {
-                    // the staging buffer of two stores ago has been read
-                    const uint32_t out = stage_out + (stores & 1u) * kOutBytes;
+                    tmem_ld_frag32(acc + column(k), v);
+                    tmem_ld_frag32(acc + (16u << 16) + column(k), v + 16);
+                } else {
+                    tmem_ld32(acc + column(k), v);
+                }
+            };
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free_bar);
+            };
+            auto store = [&](int k, const uint32_t (&v)[32]) {
+                const int t = t0 + column(k);
+                if (t >= a.m || n0 >= a.n) return;   // the same for the CTA
+                if (a.y_tma) {
+                    // the buffer was seen free before the previous store's barrier (or is new)
+                    const uint32_t dst = out + stores % C::kOutBufs * kOutBytes + frag;
                     ++stores;
-                    if (threadIdx.x == 0) bulk_wait_read<1>();
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    const uint32_t dst = out + threadIdx.x * 2u;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const uint32_t two = pack_bf16x2(__uint_as_float(v[c]) * sc.x * sc.y,
-                                                         __uint_as_float(v[c + 1]) * sc.x * sc.y);
-                        asm volatile("st.shared.b16 [%0], %1;" :: "r"(dst + c * 256u), "h"((uint16_t)two) : "memory");
-                        asm volatile("st.shared.b16 [%0], %1;" :: "r"(dst + c * 256u + 256u), "h"((uint16_t)(two >> 16))
-                                     : "memory");
+                    for (int r = 0; r < 4; ++r) {   // eight tokens
+                        uint32_t h[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            h[g] = pack_bf16x2(__uint_as_float(v[16 * (g >> 1) + 4 * r + 2 * (g & 1)]) * sc.x * sc.y,
+                                               __uint_as_float(v[16 * (g >> 1) + 4 * r + 2 * (g & 1) + 1]) * sc.x * sc.y);
+                        stmatrix_trans(dst + r * 1024u, h[0], h[1], h[2], h[3]);
                     }
                     fence_async_shared();
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    if (threadIdx.x == 0) {
-                        tma_store_3d(&a.y, out, n0, t, p.b);
+                    if (issuer) bulk_wait_read<C::kOutBufs - 2>();   // the next chunk's buffer has been read
+                    asm volatile("bar.sync %0, 64;" :: "r"(2 + (warp >> 1)) : "memory");
+                    const int x = n0 + (warp >> 1) * 64;
+                    if (issuer && x < a.n) {
+                        tma_store_3d(&a.y, dst - frag, x, t, p.b);
                         bulk_commit();
                     }
                 } else if (nn < a.n) {
@@ -489,9 +506,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     for (int c = 0; c < 32; ++c)
                         if (t + c < a.m) yp[(int64_t)(t + c) * a.y_rs] = bf16_bits(__uint_as_float(v[c]) * sc.x * sc.y);
                 }
+            };
+            if (!vote_all(wait_or_record(acc_full + 8u * buf, (n / 2u) & 1u))) break;   // the four warps leave together
+            tc_fence_after();
+            if (shared > 0) {
+                uint32_t held[C::kMaxShared][32];
+#pragma unroll
+                for (int k = 0; k < C::kMaxShared; ++k)
+                    if (k < shared) load(k, held[k]);
+                tmem_ld_wait();
+                release();
+#pragma unroll
+                for (int k = 0; k < C::kMaxShared; ++k)
+                    if (k < shared) store(k, held[k]);
+            }
+            for (int k = shared; k < chunks; ++k) {
+                uint32_t v[32];
+                load(k, v);
+                tmem_ld_wait();
+                if (shared == 0 && k == chunks - 1) release();
+                store(k, v);
             }
         }
-        if (threadIdx.x == 0) bulk_wait<0>();
+        if (issuer) bulk_wait<0>();
     }
     tc_fence_before();
     __syncthreads();
@@ -623,9 +660,9 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
         const cuuint64_t dims[3] = {(cuuint64_t)p.y.cols, (cuuint64_t)p.y.rows, (cuuint64_t)p.y.batch};
         const cuuint64_t strides[2] = {(cuuint64_t)p.y.rstride,
                                        (cuuint64_t)(p.y.batch > 1 ? p.y.bstride : p.y.rows * p.y.rstride)};
-        const cuuint32_t box[3] = {128, kOutTokens, 1}, es[3] = {1, 1, 1};
+        const cuuint32_t box[3] = {64, kOutTokens, 1}, es[3] = {1, 1, 1};
         if (encode(&a.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.y.ptr, dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
