@@ -60,6 +60,13 @@ __device__ __forceinline__ float2 output_scale(const float* ga, const float* gw,
     return make_float2((float)p, 1.0f);
 }
 
+// An accumulator times the output scale (none for MXFP8).
+template <ProductFormat kF>
+__device__ __forceinline__ float scaled(uint32_t acc, float2 sc) {
+    const float v = __uint_as_float(acc);
+    return kF == ProductFormat::kNvfp4 ? v * sc.x * sc.y : v;
+}
+
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
     return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
 }
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
                 for (int c = 0; c < kChunk; ++c) {
                     const int t = t0 + c0 + c;
                     if (t < a.m && n < a.n)
-                        y[(int64_t)t * a.y_rs] = bf16_bits(__uint_as_float(v[c]) * sc.x * sc.y);
+                        y[(int64_t)t * a.y_rs] = bf16_bits(scaled<kF>(v[c], sc));
                 }
             } else {
                 // the loads have landed and the MMAs read the ring no more
@@ -256,11 +263,12 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
 // that the pairs at work share operands in L2.
 //
-// Tensor memory: 512 columns hold three scale buffers (a step's scales are
-// copied once the MMAs of the step three before have been seen to end; with
-// two buffers that wait cost 10 to 13 % of the step) and two accumulators
-// that overlap where two of 256 columns do not fit: the epilogue takes the
-// shared columns into registers first and then lets the next tile begin.
+// Tensor memory: 512 columns hold scale buffers of a step each (three for
+// NVFP4, five for MXFP8; a buffer is filled again once the step that read it
+// has been seen to end: with two buffers that wait cost 10 to 13 % of the
+// step) and two accumulators, which overlap where two of 256 columns do not
+// fit: the epilogue takes the shared columns into registers first and then
+// lets the next tile begin.
 //
 // Output: 32 tokens at a time, TMEM fragments are transposed by stmatrix into
 // [token][64 weight rows] boxes (128-byte swizzle, no bank conflicts) and
@@ -303,11 +311,11 @@ struct PairCfg {
     static constexpr uint32_t kOutBufs = T::kFp4 ? 4u : 3u;                   // output staging buffers per warp pair
     static constexpr uint32_t kOutAt = kStages * kStage, kScalesAt = kOutAt + 2u * kOutBufs * kOutBytes;
     static constexpr uint32_t kSmem = kScalesAt + kStages * kScales + 1024u;
-    static constexpr uint32_t kScaleBufs = 3u;
+    static constexpr uint32_t kScaleBufs = T::kFp4 ? 3u : 5u;
     static constexpr uint32_t kScaleCols = 12u * T::kScaleTiles;              // per buffer: 4 weights + 8 tokens per tile
     static constexpr uint32_t kScaleAt = 512u - kScaleBufs * kScaleCols;
-    static constexpr uint32_t kAcc1 = (kScaleAt - 256u) / 32u * 32u;          // second accumulator
-    static constexpr int kMaxShared = (256 - (int)kAcc1) / 32;                // 32-column chunks in both
+    static constexpr int kMaxShared = (512 - (int)kScaleAt / 32 * 32) / 32;   // 32-column chunks in both accumulators
+    static_assert(kScaleBufs < kStages, "a scale buffer's last step still owns its barrier phase");
     static_assert(kSmem <= 232448u - 256u, "shared memory");
 };
 
@@ -342,8 +350,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-    // 32-column chunks that the two accumulators share
-    const int shared = max(0, a.tile_t - (int)C::kAcc1) / 32;
+    // the second accumulator's column, and the 32-column chunks that the two share
+    const uint32_t acc1 = min((uint32_t)a.tile_t, (C::kScaleAt - (uint32_t)a.tile_t) / 32u * 32u);
+    const int shared = (a.tile_t - (int)acc1) / 32;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kS; ++i) {
@@ -400,19 +409,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             bool ok = true;
             for (uint32_t i = first; ok && i < a.tiles; i += stride, ++n) {
                 const PairTile p = pair_tile(a, i);
-                const uint32_t buf = n & 1u, acc = tmem + buf * C::kAcc1;
+                const uint32_t buf = n & 1u, acc = tmem + buf * acc1;
                 const uint32_t tok_col = (uint32_t)(p.tt * a.tile_t % 128) / 32u;
                 // the accumulator is free: with shared columns, once the previous tile's have been read;
                 // without, once the tile before that has been read
                 if (shared > 0 && n >= 1) ok = warp_wait(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
                 if (shared == 0 && n >= 2) ok = warp_wait(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
                 if (!ok) break;
-                fence_cluster();
                 tc_fence_after();
                 for (int s = 0; s < a.steps; ++s, ++it) {
                     const uint32_t st = it % kS;
                     if (!warp_wait(full + 8u * st, (it / kS) & 1u) ||
-                        // the buffer's last scales are read no more
+                        // the scale buffer's last step has ended
                         (it >= C::kScaleBufs && !warp_wait(empty + 8u * ((it - C::kScaleBufs) % kS),
                                                            ((it - C::kScaleBufs) / kS) & 1u))) {
                         ok = false;
@@ -421,23 +429,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tc_fence_after();
                     const uint32_t at = ring + st * C::kStage, sc = scales + st * C::kScales;
                     const uint32_t sw = tmem + C::kScaleAt + it % C::kScaleBufs * C::kScaleCols;
-                    const uint32_t sx = sw + 4u * T::kScaleTiles;
                     const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
                     const int mmas = s == a.steps - 1 ? a.last_mmas : kMmasPerStep;
                     if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < T::kScaleTiles; ++j) {
-                            copy_scales<2>(sw + 4u * j, desc_scales(sc + 512u * j));
-                            copy_scales<2>(sx + 8u * j, desc_scales(sc + T::kScaleBytes + 512u * j));
-                            if (a.t_band_box == 2)
-                                copy_scales<2>(sx + 8u * j + 4u, desc_scales(sc + 2u * T::kScaleBytes + 512u * j));
-                        }
-#pragma unroll
                         for (int j = 0; j < kMmasPerStep; ++j) {
                             if (j >= mmas) break;
+                            const int tile = T::kFp4 ? j : 0;   // scale tile of the step: 4 + 8 columns
+                            const uint32_t cw = sw + 12u * tile, cx = cw + 4u;
+                            if (T::kFp4 || j == 0) {
+                                copy_scales<2>(cw, desc_scales(sc + 512u * tile));
+                                copy_scales<2>(cx, desc_scales(sc + T::kScaleBytes + 512u * tile));
+                                if (a.t_band_box == 2)
+                                    copy_scales<2>(cx + 4u, desc_scales(sc + 2u * T::kScaleBytes + 512u * tile));
+                            }
                             const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
-                            mma_block_scaled<kF, 2>(acc, dw + 2u * j, dx + 2u * j, id, sw + (T::kFp4 ? 4u * j : 0u),
-                                                    sx + (T::kFp4 ? 8u * j : 0u) + tok_col, (s | j) != 0);
+                            mma_block_scaled<kF, 2>(acc, dw + 2u * j, dx + 2u * j, id, cw, cx + tok_col, (s | j) != 0);
                         }
                         mma_commit_pair(empty + 8u * st);
                     }
@@ -450,14 +457,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else {
         uint32_t n = 0, stores = 0;
         const uint32_t row = tmem + ((uint32_t)warp << 21);
-        const bool issuer = (warp & 1) == 0 && lane == 0;
         const uint32_t out = ring + C::kOutAt + (uint32_t)(warp >> 1) * C::kOutBufs * kOutBytes;
         // this lane's stmatrix row: token lane % 8 of eight, weight rows 8 (lane / 8) .. + 7 of the warp's 32
         const uint32_t c8 = (uint32_t)lane & 7u;
         const uint32_t frag = c8 * 128u + (((uint32_t)(warp & 1) * 4u + ((uint32_t)lane >> 3)) ^ c8) * 16u;
         for (uint32_t i = first; i < a.tiles; i += stride, ++n) {
             const PairTile p = pair_tile(a, i);
-            const uint32_t buf = n & 1u, acc = row + buf * C::kAcc1, free_bar = cluster_addr(acc_free + 8u * buf, 0);
+            const uint32_t buf = n & 1u, acc = row + buf * acc1, free_bar = cluster_addr(acc_free + 8u * buf, 0);
             const int n0 = (p.wt * 2 + (int)rank) * 128, t0 = p.tt * a.tile_t, chunks = a.tile_t / 32;
             const float2 sc = output_scale(a.gt, a.gw, p.b);
             const int nn = n0 + warp * 32 + lane;
@@ -475,36 +481,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(free_bar);
+                if (lane == 0) mbar_arrive_cluster_relaxed(free_bar);
             };
             auto store = [&](int k, const uint32_t (&v)[32]) {
                 const int t = t0 + column(k);
                 if (t >= a.m || n0 >= a.n) return;   // the same for the CTA
                 if (a.y_tma) {
                     // the buffer was seen free before the previous store's barrier (or is new)
-                    const uint32_t dst = out + stores % C::kOutBufs * kOutBytes + frag;
+                    const uint32_t box = out + stores % C::kOutBufs * kOutBytes, dst = box + frag;
                     ++stores;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {   // eight tokens
                         uint32_t h[4];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            h[g] = pack_bf16x2(__uint_as_float(v[16 * (g >> 1) + 4 * r + 2 * (g & 1)]) * sc.x * sc.y,
-                                               __uint_as_float(v[16 * (g >> 1) + 4 * r + 2 * (g & 1) + 1]) * sc.x * sc.y);
+                        for (int g = 0; g < 4; ++g) {
+                            const int e = 16 * (g >> 1) + 4 * r + 2 * (g & 1);
+                            h[g] = pack_bf16x2(scaled<kF>(v[e], sc), scaled<kF>(v[e + 1], sc));
+                        }
                         stmatrix_trans(dst + r * 1024u, h[0], h[1], h[2], h[3]);
                     }
                     fence_async_shared();
-                    if (issuer) bulk_wait_read<C::kOutBufs - 2>();   // the next chunk's buffer has been read
+                    const bool first_warp = (warp & 1) == 0;   // of the pair: its elected lane issues
+                    if (first_warp && elect_one()) bulk_wait_read<C::kOutBufs - 2>();   // the next buffer has been read
+                    __syncwarp();
                     asm volatile("bar.sync %0, 64;" :: "r"(2 + (warp >> 1)) : "memory");
                     const int x = n0 + (warp >> 1) * 64;
-                    if (issuer && x < a.n) {
-                        tma_store_3d(&a.y, dst - frag, x, t, p.b);
+                    if (first_warp && x < a.n && elect_one()) {
+                        tma_store_3d(&a.y, box, x, t, p.b);
                         bulk_commit();
                     }
+                    __syncwarp();
                 } else if (nn < a.n) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
-                        if (t + c < a.m) yp[(int64_t)(t + c) * a.y_rs] = bf16_bits(__uint_as_float(v[c]) * sc.x * sc.y);
+                        if (t + c < a.m) yp[(int64_t)(t + c) * a.y_rs] = bf16_bits(scaled<kF>(v[c], sc));
                 }
             };
             if (!vote_all(wait_or_record(acc_full + 8u * buf, (n / 2u) & 1u))) break;   // the four warps leave together
@@ -528,7 +538,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 store(k, v);
             }
         }
-        if (issuer) bulk_wait<0>();
+        if ((warp & 1) == 0 && elect_one()) bulk_wait<0>();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -611,17 +622,18 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tokens per tile of the pair kernel: the least (waves of tiles) x (columns
-// of a tile + a fixed cost in columns).  kTileCost is the measured cost of a
-// tile's start and of its weight operand.
-constexpr int kTileCost = 48;
-int pair_tile_tokens(int64_t m, int64_t w_tiles, int64_t batch, int64_t pairs) {
+// Tokens per tile of the pair kernel: the fewest (waves of tiles) x (time of
+// a tile).  A step's time goes with the bytes that it brings from L2 (256
+// weight rows, the tile's tokens, scales worth 24 rows), measured as 0.39 /
+// 0.35 / 0.30 us for 256 / 192 / 128 tokens; a tile's start and the part of
+// its epilogue that nothing hides cost about two steps.
+int pair_tile_tokens(int64_t m, int64_t w_tiles, int64_t batch, int64_t pairs, int64_t steps) {
     int best = 256;
     int64_t best_cost = -1;
     for (int t = 256; t >= 32; t -= 32) {
         if (t % 64 != 0 && m > t) continue;
         const int64_t tiles = batch * w_tiles * ((m + t - 1) / t);
-        const int64_t cost = (tiles + pairs - 1) / pairs * (t + kTileCost);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (steps * (256 + t + 24) + 1000);
         if (best_cost < 0 || cost < best_cost) {
             best = t;
             best_cost = cost;
@@ -642,7 +654,8 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
     const int64_t col_tiles = mma_scale_col_tiles(p.k / (T::kFp4 ? 16 : 32));
     const int64_t pairs = sm_count(current_device()) / 2, w_tiles = (p.w.rows + 255) / 256;
     PairArgs a;
-    a.tile_t = pair_tile_tokens(p.a.rows, w_tiles, p.a.batch, pairs);
+    a.steps = (int)((row_bytes + kStepBytes - 1) / kStepBytes);
+    a.tile_t = pair_tile_tokens(p.a.rows, w_tiles, p.a.batch, pairs, a.steps);
     a.t_band_box = 128 % a.tile_t == 0 ? 1 : 2;
     const int64_t t_tiles = (p.a.rows + a.tile_t - 1) / a.tile_t;
     a.w_bands = (int)((p.w.rows + 127) / 128);
@@ -673,7 +686,6 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
     a.y_rs = p.y.rstride / 2;
     a.n = (int)p.w.rows;
     a.m = (int)p.a.rows;
-    a.steps = (int)((row_bytes + kStepBytes - 1) / kStepBytes);
     a.last_mmas = (int)((row_bytes - (int64_t)(a.steps - 1) * kStepBytes + 31) / 32);
     a.w_tiles = (uint32_t)w_tiles;
     a.t_tiles = (uint32_t)t_tiles;

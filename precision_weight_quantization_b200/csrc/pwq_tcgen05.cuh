@@ -202,11 +202,14 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 
 // ---------------------------------------------------------------- clusters
 
-// Arrives on a barrier of any CTA of the cluster (address in the cluster window).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+// Arrives on a barrier of any CTA of the cluster (address in the cluster
+// window) to say that this warp's TMEM loads have ended: registers hold the
+// values, no memory is published, so the arrival is relaxed and the
+// tcgen05 fences on both sides give the order (a releasing arrival here
+// costs about 1000 clocks).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
