@@ -13,19 +13,19 @@
 // y never reaches memory.
 //
 // y is the BF16 nearest to the exact product, so that codes do not depend on
-// the order of a sum: the squares are summed in 64 bits, h * weight is exact
-// in FP32 (8 + 8 significant bits), and only a product that lies within two
-// FP32 units of a BF16 tie (5 in 65536 of them) is formed again in 64 bits.
-// That costs 1 FP64 operation and about 4 integer ones per element, hidden
-// behind HBM.
+// the order of a sum.  The squares are summed in 64 bits.  With rstd = m 2^E,
+// h 2^E is exact, (h 2^E) weight is exact (8 + 8 significant bits), and the
+// one FP32 rounding of its product with m is off by less than two units; so
+// only a product within two units of a BF16 tie (5 in 65536) is formed again
+// in 64 bits.  The kernel is bound by HBM when it issues fewer than about 20
+// instructions per element: hence the packed additions and products, and the
+// tie test on eight low halves at once.
 #include <algorithm>
 
 #include "pwq_internal.h"
 
 namespace pwq {
 namespace {
-
-constexpr int kVec = 4;   // 8-element vectors per thread, all loaded before any is used
 
 enum class NormOut { kMxfp8, kNvfp4, kMxfp8Fake, kNvfp4Fake };
 
@@ -48,29 +48,27 @@ struct NormArgs {
     uint64_t pad_words;          // 4-byte words of those rows over all slabs
 };
 
-// h^2 summed in 64 bits: the BF16 h widened to 64 bits by moving its
-// exponent and mantissa (a zero becomes 2^-127, which no sum notices beside eps).
-__device__ __forceinline__ double widen_bits(uint32_t f32_bits) {
-    return __hiloint2double((int)(((f32_bits & 0x7fffffffu) >> 3) + 0x38000000u), 0);
+// bf16(x + residual) of BF16 pairs in one rounding.  (The same value as the
+// FP32 sum rounded to BF16: an FP32 sum of two BF16 is exact, or its smaller
+// term is too small to reach a tie.)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
+__device__ __forceinline__ uint4 add_bf16(uint4 a, uint4 b) {
+    return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
+}
+
 __device__ __forceinline__ double add_squares(double s, uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const double lo = widen_bits(w[i] << 16), hi = widen_bits(w[i] & 0xffff0000u);
+        const double lo = (double)bf16_lo(w[i]), hi = (double)bf16_hi(w[i]);
         s = __fma_rn(lo, lo, s);
         s = __fma_rn(hi, hi, s);
     }
     return s;
-}
-
-__device__ __forceinline__ uint4 add_bf16(uint4 a, uint4 b) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = pack_bf16x2(__fadd_rn(bf16_lo(x[i]), bf16_lo(y[i])), __fadd_rn(bf16_hi(x[i]), bf16_hi(y[i])));
-    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // A 64-bit value as FP32 that rounds to the same BF16: the nearest FP32,
@@ -83,30 +81,56 @@ __device__ __forceinline__ float narrow_for_bf16(float h, float w, double rstd) 
     return __uint_as_float(__float_as_uint(f) + (fabs(t) > fabs(back) ? 1u : 0xffffffffu));
 }
 
-// y = bf16(h rstd weight) of 8 elements; rh = fl(rstd).
-__device__ __forceinline__ uint4 normalise(uint4 hv, uint4 wv, float rh, double rstd) {
+// The row's rstd for normalise(): hs = 2^E with E = max(exponent of rstd,
+// -16) (h 2^E is then a multiple of 2^-149, exact), m = fl(rstd 2^-E).
+// Rows whose rstd is below 2^-60 form every product in 64 bits.
+struct RowScale {
+    double rstd;
+    uint64_t hs2, m2;   // {hs, hs}, {m, m}
+    bool wide;
+};
+__device__ __forceinline__ RowScale row_scale(double rstd) {
+    RowScale r;
+    r.rstd = rstd;
+    const int E = max((__double2hiint(rstd) >> 20) - 1023, -16);
+    const float hs = __uint_as_float((uint32_t)(E + 127) << 23);
+    const float m = (float)(rstd * __hiloint2double((1023 - E) << 20, 0));
+    r.hs2 = f32x2(hs, hs);
+    r.m2 = f32x2(m, m);
+    r.wide = rstd < 0x1p-60;
+    return r;
+}
+
+__device__ __noinline__ uint4 normalise_wide(uint4 hv, uint4 wv, double rstd) {
     const uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, w[4] = {wv.x, wv.y, wv.z, wv.w};
-    float q[8];
-    bool near_tie = false;
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = i & 1 ? bf16_hi(h[i >> 1]) : bf16_lo(h[i >> 1]);
-        const float b = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-        q[i] = __fmul_rn(__fmul_rn(a, b), rh);
-        const uint32_t u = __float_as_uint(q[i]);
-        // within two FP32 units of a tie; or so small or large (2^-96, infinite) that a factor left the normal range
-        near_tie |= ((u - 0x7ffeu) & 0xffffu) <= 4u;
-        near_tie |= ((u & 0x7fffffffu) - 0x0f800000u) >= 0x70000000u;
-    }
-    if (near_tie) {
+    for (int i = 0; i < 4; ++i)
+        o[i] = pack_bf16x2(narrow_for_bf16(bf16_lo(h[i]), bf16_lo(w[i]), rstd),
+                           narrow_for_bf16(bf16_hi(h[i]), bf16_hi(w[i]), rstd));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// y = bf16(h rstd weight) of 8 elements.
+__device__ __forceinline__ uint4 normalise(uint4 hv, uint4 wv, const RowScale& rs) {
+    const uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, w[4] = {wv.x, wv.y, wv.z, wv.w};
+    uint32_t o[4], low[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[2 * i] = narrow_for_bf16(bf16_lo(h[i]), bf16_lo(w[i]), rstd);
-            q[2 * i + 1] = narrow_for_bf16(bf16_hi(h[i]), bf16_hi(w[i]), rstd);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t hf = f32x2_bits(h[i] << 16, h[i] & 0xffff0000u), wf = f32x2_bits(w[i] << 16, w[i] & 0xffff0000u);
+        const float2 q = f32x2_split(mul_f32x2(mul_f32x2(mul_f32x2(hf, rs.hs2), wf), rs.m2));
+        o[i] = pack_bf16x2(q.x, q.y);
+        // low halves + 0x8002: 0 .. 4 within two units of a tie; the carry from the lower into the upper
+        // half adds at most 1, so up to 5 counts
+        low[i] = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x5410) + 0x80028002u;
     }
-    return make_uint4(pack_bf16x2(q[0], q[1]), pack_bf16x2(q[2], q[3]), pack_bf16x2(q[4], q[5]),
-                      pack_bf16x2(q[6], q[7]));
+    uint32_t lo = __vminu2(__vminu2(low[0], low[1]), __vminu2(low[2], low[3]));
+    lo = min(lo & 0xffffu, lo >> 16);
+    // an infinite y: the product may have left FP32 although the value did not
+    const uint32_t hi = hmax_abs(hmax_abs(o[0], o[1]), hmax_abs(o[2], o[3])) & 0x7fff7fffu;
+    const bool inf = (hi & 0xffffu) >= 0x7f80u || hi >= 0x7f800000u;
+    if (lo <= 5u || inf || rs.wide) return normalise_wide(hv, wv, rs.rstd);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -128,17 +152,19 @@ __device__ __forceinline__ void store_scale(const NormArgs& a, uint32_t r, uint3
     }
 }
 
-// kThreads threads per row, one row per CTA.  Four (MXFP8) or two (NVFP4)
-// neighbouring lanes hold a block: 16-byte loads stay coalesced and the
-// block maximum takes one or two shuffles.
-template <NormOut kOut, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormArgs a) {
+// One row per CTA, kVec 8-element vectors per thread, all loaded before any
+// is used: many rows take four (fewer warps per row, more rows in flight),
+// few rows one (the row's latency counts).  Four (MXFP8) or two (NVFP4)
+// neighbouring lanes hold a block: 16-byte loads stay coalesced and the block
+// maximum takes one or two shuffles.
+template <NormOut kOut, int kVec, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kMx = kOut == NormOut::kMxfp8 || kOut == NormOut::kMxfp8Fake;
     constexpr bool kFake = kOut == NormOut::kMxfp8Fake || kOut == NormOut::kNvfp4Fake;
-    constexpr int kWarps = kThreads / 32;
+    const int threads = (int)blockDim.x;
     if (!kFake && blockIdx.x >= a.row_ctas) {   // zero scales of the rows that pad the last band
-        for (uint64_t i = (uint64_t)(blockIdx.x - a.row_ctas) * kThreads + threadIdx.x; i < a.pad_words;
-             i += (uint64_t)(gridDim.x - a.row_ctas) * kThreads) {
+        for (uint64_t i = (uint64_t)(blockIdx.x - a.row_ctas) * threads + threadIdx.x; i < a.pad_words;
+             i += (uint64_t)(gridDim.x - a.row_ctas) * threads) {
             const uint64_t row = i / a.sf_ct;
             const uint32_t ct = (uint32_t)(i - row * a.sf_ct);
             const uint32_t b = (uint32_t)(row / a.pad_rows), m = a.rows.d + (uint32_t)(row - (uint64_t)b * a.pad_rows);
@@ -146,49 +172,45 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         }
         return;
     }
-    __shared__ double part[kWarps];
+    __shared__ double part[kMaxThreads / 32];
     const uint32_t r = blockIdx.x;
     const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
     const int lane = threadIdx.x & 31;
-    const char* x = a.x.ptr + (int64_t)b * a.x.bstride + (int64_t)m * a.x.rstride;
-    uint4 v[kVec];
+    const char* x = a.x.ptr + (int64_t)b * a.x.bstride + (int64_t)m * a.x.rstride + 16 * threadIdx.x;
+    const int step = 16 * threads;   // bytes between a thread's vectors
+    uint4 v[kVec], wv[kVec];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int k = i * kThreads + (int)threadIdx.x;
-        v[i] = k < a.vecs ? ld_stream_v4(x + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < kVec; ++i)
+        v[i] = i * threads + (int)threadIdx.x < a.vecs ? ld_stream_v4(x + i * step) : make_uint4(0u, 0u, 0u, 0u);
     if (a.res.ptr) {
-        const char* res = a.res.ptr + (int64_t)b * a.res.bstride + (int64_t)m * a.res.rstride;
-        char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride;
+        const char* res = a.res.ptr + (int64_t)b * a.res.bstride + (int64_t)m * a.res.rstride + 16 * threadIdx.x;
+        char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride + 16 * threadIdx.x;
         uint4 u[kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int k = i * kThreads + (int)threadIdx.x;
-            u[i] = k < a.vecs ? ld_stream_v4(res + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int i = 0; i < kVec; ++i)
+            u[i] = i * threads + (int)threadIdx.x < a.vecs ? ld_stream_v4(res + i * step) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int k = i * kThreads + (int)threadIdx.x;
             v[i] = add_bf16(v[i], u[i]);
-            if (k < a.vecs) st_v4(h + 16 * (int64_t)k, v[i]);
+            if (i * threads + (int)threadIdx.x < a.vecs) st_v4(h + i * step, v[i]);
         }
     }
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-        if (i * kThreads + (int)threadIdx.x < a.vecs) s = add_squares(s, v[i]);
+    for (int i = 0; i < kVec; ++i) {
+        const int k = i * threads + (int)threadIdx.x;
+        wv[i] = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
+        s = add_squares(s, v[i]);
+    }
     s = warp_sum(s);
-    if (kWarps > 1) {
+    if (threads > 32) {
         if (lane == 0) part[threadIdx.x >> 5] = s;
         __syncthreads();
         s = 0.0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) s += part[i];   // the same order in every thread
+        for (int i = 0; i < threads / 32; ++i) s += part[i];   // the same order in every thread
     }
-    const double rstd = 1.0 / sqrt(s / (double)(8 * a.vecs) + a.eps);
-    const float rf = (float)rstd;
-    const float rh = rf < 0x1p-100f ? 0.0f : rf;   // huge rows: every product takes the 64-bit path
-    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rf;
+    const RowScale rs = row_scale(1.0 / sqrt(s / (double)(8 * a.vecs) + a.eps));
+    if (a.rstd && threadIdx.x == 0) a.rstd[r] = (float)rs.rstd;
 
     float gs = 0.0f, g6 = 0.0f, r6 = 0.0f;
     bool fast6 = false;
@@ -202,32 +224,32 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     char* out = a.out.ptr + (int64_t)b * a.out.bstride + (int64_t)m * a.out.rstride;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        if (i * kThreads >= a.vecs) break;   // uniform: shuffles below take whole warps
-        const int k = i * kThreads + (int)threadIdx.x;
+        if (i * threads >= a.vecs) break;   // uniform: shuffles below take whole warps
+        const int k = i * threads + (int)threadIdx.x;
         const bool on = k < a.vecs;
-        uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if (on) y = normalise(v[i], __ldg(a.weight + k), rh, rstd);
+        const uint4 y = normalise(v[i], wv[i], rs);   // zeros past the row
         uint32_t mw = amax_word8(y);
         mw = hmax_abs(mw, __shfl_xor_sync(0xffffffffu, mw, 1));
         if (kMx) mw = hmax_abs(mw, __shfl_xor_sync(0xffffffffu, mw, 2));
         mw &= 0x7fff7fffu;
         const uint32_t amax = max(mw & 0xffffu, mw >> 16);
         if (kMx) {
-            const int e = ue8m0_exponent(amax);
-            float q[8];
-            const float inv = exp2i(-e);
+            // scale byte e + 127 with e = min{k : amax <= 448 2^k}: 448 = 1.75 * 2^8, so a mantissa above .75
+            // (96 of 128) carries into the exponent; below 2^-127 (zero and subnormal amax) the byte is 0
+            const int byte8 = max((int)((amax + 31u) >> 7) - 8, 0);
+            const float inv = __uint_as_float((uint32_t)(254 - byte8) << 23);   // 2^-e
+            const uint64_t inv2 = f32x2(inv, inv);
             const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            float2 q[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                q[2 * j] = __fmul_rn(bf16_lo(w[j]), inv);
-                q[2 * j + 1] = __fmul_rn(bf16_hi(w[j]), inv);
-            }
-            const uint2 c = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+            for (int j = 0; j < 4; ++j)
+                q[j] = f32x2_split(mul_f32x2(f32x2_bits(w[j] << 16, w[j] & 0xffff0000u), inv2));
+            const uint2 c = make_uint2(e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y), e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
             if (kFake) {
-                if (on) st_v4(out + 16 * (int64_t)k, fp8_dequant8(c, exp2i(e)));
+                if (on) st_v4(out + 16 * (int64_t)k, fp8_dequant8(c, exp2i(byte8 - 127)));
             } else {
                 if (on) st_v2(out + 8 * (int64_t)k, c);
-                const uint32_t byte = on ? (uint32_t)(e + 127) : 0u;
+                const uint32_t byte = on ? (uint32_t)byte8 : 0u;
                 uint32_t word = byte;
 #pragma unroll
                 for (int j = 1; j < 4; ++j) word |= __shfl_down_sync(0xffffffffu, byte, 4 * j) << (8 * j);
@@ -283,39 +305,55 @@ __device__ __forceinline__ float warp_sum_f(float v) {
     return v;
 }
 
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ float part[2][kWarps];
+// The next row's loads are in flight while this row is reduced and written.
+template <int kVec, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+    __shared__ float part[2][kMaxThreads / 32];
+    const int threads = (int)blockDim.x, step = 16 * threads;
+    const bool has_dh = a.dh.ptr != nullptr;
+    const float inv_d = __fdiv_rn(1.0f, (float)(8 * a.vecs));
     float dw[kVec][8];
+    uint4 wv[kVec];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < kVec; ++i) {
+        const int k = i * threads + (int)threadIdx.x;
+        wv[i] = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-    int flip = 0;
-    for (uint32_t r = blockIdx.x; r < a.total_rows; r += gridDim.x, flip ^= 1) {
+    }
+    uint4 ng[kVec], nh[kVec], nd[kVec];
+    float nr = 0.0f;
+    auto fetch = [&](uint32_t r) {
         const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
-        const char* dy = a.dy.ptr + (int64_t)b * a.dy.bstride + (int64_t)m * a.dy.rstride;
-        const char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride;
-        const char* dh = a.dh.ptr ? a.dh.ptr + (int64_t)b * a.dh.bstride + (int64_t)m * a.dh.rstride : nullptr;
-        char* dx = a.dx.ptr + (int64_t)b * a.dx.bstride + (int64_t)m * a.dx.rstride;
-        const float rstd = __ldg(a.rstd + r);
-        uint4 vg[kVec], vh[kVec], vd[kVec];
+        const char* dy = a.dy.ptr + (int64_t)b * a.dy.bstride + (int64_t)m * a.dy.rstride + 16 * threadIdx.x;
+        const char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride + 16 * threadIdx.x;
+        const char* dh = a.dh.ptr + (int64_t)b * a.dh.bstride + (int64_t)m * a.dh.rstride + 16 * threadIdx.x;
+        nr = __ldg(a.rstd + r);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int k = i * kThreads + (int)threadIdx.x;
-            const bool on = k < a.vecs;
-            vg[i] = on ? ld_stream_v4(dy + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
-            vh[i] = on ? ld_stream_v4(h + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
-            vd[i] = on && dh ? ld_stream_v4(dh + 16 * (int64_t)k) : make_uint4(0u, 0u, 0u, 0u);
+            const bool on = i * threads + (int)threadIdx.x < a.vecs;
+            ng[i] = on ? ld_stream_v4(dy + i * step) : make_uint4(0u, 0u, 0u, 0u);
+            nh[i] = on ? ld_stream_v4(h + i * step) : make_uint4(0u, 0u, 0u, 0u);
+            nd[i] = on && has_dh ? ld_stream_v4(dh + i * step) : make_uint4(0u, 0u, 0u, 0u);
         }
+    };
+    if (blockIdx.x < a.total_rows) fetch(blockIdx.x);
+    int flip = 0;
+    for (uint32_t r = blockIdx.x; r < a.total_rows; r += gridDim.x, flip ^= 1) {
+        uint4 vg[kVec], vh[kVec], vd[kVec];
+        const float rstd = nr;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            vg[i] = ng[i];
+            vh[i] = nh[i];
+            vd[i] = nd[i];
+        }
+        if (r + gridDim.x < a.total_rows) fetch(r + gridDim.x);
         float c = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int k = i * kThreads + (int)threadIdx.x;
-            const uint4 wv = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
-            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
+            const uint32_t w[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float t0 = bf16_lo(g[j]) * (bf16_lo(hh[j]) * rstd), t1 = bf16_hi(g[j]) * (bf16_hi(hh[j]) * rstd);
@@ -326,21 +364,20 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const __grid_constan
             }
         }
         c = warp_sum_f(c);
-        if (kWarps > 1) {
+        if (threads > 32) {
             if ((threadIdx.x & 31) == 0) part[flip][threadIdx.x >> 5] = c;
             __syncthreads();   // one barrier a row: the two halves of `part` alternate
             c = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) c += part[flip][i];
+            for (int i = 0; i < threads / 32; ++i) c += part[flip][i];
         }
-        c = __fdiv_rn(c, (float)(8 * a.vecs));
+        c *= inv_d;
+        const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
+        char* dx = a.dx.ptr + (int64_t)b * a.dx.bstride + (int64_t)m * a.dx.rstride + 16 * threadIdx.x;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int k = i * kThreads + (int)threadIdx.x;
-            if (k >= a.vecs) continue;
-            const uint4 wv = __ldg(a.weight + k);
+            if (i * threads + (int)threadIdx.x >= a.vecs) continue;
             const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
-            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w}, d[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
+            const uint32_t w[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w}, d[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -348,14 +385,14 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const __grid_constan
                 const float e1 = __fmaf_rn(bf16_hi(hh[j]) * rstd, -c, bf16_hi(g[j]) * bf16_hi(w[j]));
                 o[j] = pack_bf16x2(__fmaf_rn(e0, rstd, bf16_lo(d[j])), __fmaf_rn(e1, rstd, bf16_hi(d[j])));
             }
-            st_v4(dx + 16 * (int64_t)k, make_uint4(o[0], o[1], o[2], o[3]));
+            st_v4(dx + i * step, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
     if (a.parts) {
         float* p = a.parts + (int64_t)blockIdx.x * a.vecs * 8;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int k = i * kThreads + (int)threadIdx.x;
+            const int k = i * threads + (int)threadIdx.x;
             if (k >= a.vecs) continue;
             float* q = p + 8 * (int64_t)k;
             st_v4(q, make_uint4(__float_as_uint(dw[i][0]), __float_as_uint(dw[i][1]), __float_as_uint(dw[i][2]),
@@ -387,31 +424,32 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* parts, i
     }
 }
 
-// Threads per row: the fewest that hold the row in kVec vectors each.
-int norm_threads(int64_t D) {
-    int t = 32;
-    while ((int64_t)t * kVec * 8 < D) t *= 2;
-    return t;
-}
+// Threads per row: the fewest whole warps that hold it in `vec` vectors each.
+int norm_threads(int64_t D, int vec) { return (int)((D / 8 + 32 * vec - 1) / (32 * vec)) * 32; }
 
-template <NormOut kOut>
+template <NormOut kOut, int kVec, int kMaxThreads>
 cudaError_t launch_norm_out(const NormArgs& a, int threads, cudaStream_t s) {
     const unsigned pads = a.pad_words ? (unsigned)std::min<uint64_t>((a.pad_words + threads - 1) / threads, 128) : 0u;
-    const unsigned grid = a.row_ctas + pads;
-    switch (threads) {
-        case 32: norm_kernel<kOut, 32><<<grid, 32, 0, s>>>(a); break;
-        case 64: norm_kernel<kOut, 64><<<grid, 64, 0, s>>>(a); break;
-        case 128: norm_kernel<kOut, 128><<<grid, 128, 0, s>>>(a); break;
-        case 256: norm_kernel<kOut, 256><<<grid, 256, 0, s>>>(a); break;
-        case 512: norm_kernel<kOut, 512><<<grid, 512, 0, s>>>(a); break;
-        default: norm_kernel<kOut, 1024><<<grid, 1024, 0, s>>>(a); break;
-    }
+    norm_kernel<kOut, kVec, kMaxThreads><<<a.row_ctas + pads, threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-int norm_bwd_grid(int64_t rows, int threads) {
-    const int per_sm = std::max(1, std::min(16, 512 / threads));
-    return persistent_grid(rows, per_sm);
+template <NormOut kOut>
+cudaError_t launch_norm_kind(const NormArgs& a, cudaStream_t s) {
+    const int64_t D = 8 * (int64_t)a.vecs;
+    // few rows leave SMs idle either way: spread each over four times the threads
+    if (D <= 8192 && a.total_rows <= (uint32_t)sm_count(current_device()))
+        return launch_norm_out<kOut, 1, 1024>(a, norm_threads(D, 1), s);
+    if (D <= 8192) return launch_norm_out<kOut, 4, 256>(a, norm_threads(D, 4), s);
+    return launch_norm_out<kOut, 4, 1024>(a, norm_threads(D, 4), s);
+}
+
+// Vectors per thread of the backward pass: two while a CTA's threads hold the row.
+int norm_bwd_vec(int64_t D) { return D <= 16384 ? 2 : 4; }
+
+int norm_bwd_grid(int64_t rows, int64_t D) {
+    const int threads = norm_threads(D, norm_bwd_vec(D));
+    return persistent_grid(rows, std::max(1, std::min(16, 640 / threads)));
 }
 
 }  // namespace
@@ -438,15 +476,12 @@ cudaError_t launch_norm(const Norm& n, cudaStream_t s) {
     a.row_ctas = a.total_rows;
     a.pad_rows = n.scale_mma && !n.fake ? (uint32_t)((128 - n.x.rows % 128) % 128) : 0u;
     a.pad_words = (uint64_t)n.x.batch * a.pad_rows * a.sf_ct;
-    const int threads = norm_threads(n.x.cols);
-    if (n.fp4) return n.fake ? launch_norm_out<NormOut::kNvfp4Fake>(a, threads, s)
-                             : launch_norm_out<NormOut::kNvfp4>(a, threads, s);
-    return n.fake ? launch_norm_out<NormOut::kMxfp8Fake>(a, threads, s)
-                  : launch_norm_out<NormOut::kMxfp8>(a, threads, s);
+    if (n.fp4) return n.fake ? launch_norm_kind<NormOut::kNvfp4Fake>(a, s) : launch_norm_kind<NormOut::kNvfp4>(a, s);
+    return n.fake ? launch_norm_kind<NormOut::kMxfp8Fake>(a, s) : launch_norm_kind<NormOut::kMxfp8>(a, s);
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
-    return ((size_t)norm_bwd_grid(rows, norm_threads(D)) * (size_t)D * 4 + 255) / 256 * 256;
+    return ((size_t)norm_bwd_grid(rows, D) * (size_t)D * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
@@ -461,15 +496,12 @@ cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
     a.rows = make_fastdiv((uint32_t)n.h.rows);
     a.total_rows = (uint32_t)(n.h.batch * n.h.rows);
     a.vecs = (int)(n.h.cols / 8);
-    const int threads = norm_threads(n.h.cols), grid = norm_bwd_grid(a.total_rows, threads);
-    switch (threads) {
-        case 32: norm_bwd_kernel<32><<<grid, 32, 0, s>>>(a); break;
-        case 64: norm_bwd_kernel<64><<<grid, 64, 0, s>>>(a); break;
-        case 128: norm_bwd_kernel<128><<<grid, 128, 0, s>>>(a); break;
-        case 256: norm_bwd_kernel<256><<<grid, 256, 0, s>>>(a); break;
-        case 512: norm_bwd_kernel<512><<<grid, 512, 0, s>>>(a); break;
-        default: norm_bwd_kernel<1024><<<grid, 1024, 0, s>>>(a); break;
-    }
+    const int64_t cols = n.h.cols;
+    const int vec = norm_bwd_vec(cols), threads = norm_threads(cols, vec), grid = norm_bwd_grid(a.total_rows, cols);
+    if (vec == 2 && threads <= 256) norm_bwd_kernel<2, 256><<<grid, threads, 0, s>>>(a);
+    else if (vec == 2 && threads <= 512) norm_bwd_kernel<2, 512><<<grid, threads, 0, s>>>(a);
+    else if (vec == 2) norm_bwd_kernel<2, 1024><<<grid, threads, 0, s>>>(a);
+    else norm_bwd_kernel<4, 1024><<<grid, threads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !n.dweight) return e;
     const int D = (int)n.h.cols;
