@@ -580,14 +580,18 @@ def nvfp4_quant_grouped_mma(groups: Sequence[Sequence[torch.Tensor]], out=None, 
 
 # ---------------------------------------------------------------- block-scaled products
 
-def _launch(t: torch.Tensor, name: str, *args):
-    """Calls the library on t's device and its current stream (the library launches on the current device)."""
+def _on(t: torch.Tensor, f, *args):
+    """f(*args) with t's device current."""
     index = t.device.index
     if torch.cuda.current_device() == index:
-        status = getattr(lib, name)(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = getattr(lib, name)(*args, _raw_stream(index))
+        return f(*args)
+    with torch.cuda.device(index):
+        return f(*args)
+
+
+def _launch(t: torch.Tensor, name: str, *args):
+    """Calls the library on t's device and its current stream (the library launches on the current device)."""
+    status = _on(t, getattr(lib, name), *args, _raw_stream(t.device.index))
     if status:
         check(status, name)
 
@@ -777,21 +781,30 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
     px, _, _, dhh, _ = _norm_inputs(h, weight, None, None)
     if rstd.shape != h.shape[:-1]:
         raise ValueError("rstd must have shape %s" % (tuple(h.shape[:-1]),))
-    if out is None:
-        out = torch.empty(h.shape, dtype=torch.bfloat16, device=h.device)
-    _check_dtype(out, (torch.bfloat16,), "out")
+    if out is not None:
+        _check_dtype(out, (torch.bfloat16,), "out")
+    _floats(rstd, dhh.batch * dhh.rows, "rstd")
     _same_device(h, dy, weight, rstd, dh, out)
-    dw, ws, n = None, None, 0
-    if need_dweight:
-        with torch.cuda.device(h.device):     # the size depends on the device
-            n = max(int(lib.rms_norm_backward_workspace_size(px)), 256)
-        dw = torch.empty(dhh.cols, dtype=dweight_dtype, device=h.device)
-        ws = torch.empty(n, dtype=torch.uint8, device=h.device)
+    return _norm_backward(dy, h, weight, rstd, dh, dweight_dtype if need_dweight else None, out)
+
+
+def _norm_backward(dy, h, weight, rstd, dh, dweight_dtype, out=None):
+    """rms_norm_backward of checked arguments (dweight_dtype None: no dweight)."""
+    dev = h.device
+    if out is None:
+        out = torch.empty(h.shape, dtype=torch.bfloat16, device=dev)
+    ph = ctypes.byref(_desc(h, "h"))
+    dw = None
+    pw = pws = None
+    n = 0
+    if dweight_dtype is not None:
+        n = max(_on(h, lib.rms_norm_backward_workspace_size, ph), 256)      # depends on the device's SM count
+        dw = torch.empty(h.shape[-1], dtype=dweight_dtype, device=dev)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        pw, pws = dw.data_ptr(), ws.data_ptr()
     _launch(h, "rms_norm_backward", ctypes.byref(_desc(dy, "dy")),
-            ctypes.byref(_desc(dh, "dh")) if dh is not None else None, px, weight.data_ptr(),
-            _floats(rstd, dhh.batch * dhh.rows, "rstd"), ctypes.byref(_desc(out, "out")),
-            dw.data_ptr() if need_dweight else None, int(dweight_dtype == torch.bfloat16),
-            ws.data_ptr() if need_dweight else None, n)
+            ctypes.byref(_desc(dh, "dh")) if dh is not None else None, ph, weight.data_ptr(), rstd.data_ptr(),
+            ctypes.byref(_desc(out, "out")), pw, int(dweight_dtype == torch.bfloat16), pws, n)
     return out, dw
 
 
@@ -804,22 +817,27 @@ class _RMSNormSTE(torch.autograd.Function):
         return (y, h) if residual is not None else y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dh=None):
-        h, weight, rstd = ctx.saved_tensors
+        if torch.is_grad_enabled():     # create_graph: the gradient below records no graph
+            raise RuntimeError("rms_norm_fake_quant_ste has no second derivative")
         need_x, need_w, need_r = ctx.needs_input_grad[:3]
         dx, dw = dh, None
         if dy is not None:
-            dx, dw = rms_norm_backward(_last_contiguous(dy), h, weight, rstd,
-                                       dh=_last_contiguous(dh) if dh is not None else None,
-                                       dweight_dtype=torch.bfloat16, need_dweight=need_w)
+            h, weight, rstd = ctx.saved_tensors
+            dx, dw = _norm_backward(_last_contiguous(dy), h, weight, rstd,
+                                    _last_contiguous(dh) if dh is not None else None,
+                                    torch.bfloat16 if need_w else None)
         return dx if need_x else None, dw, dx if need_r else None, None, None, None
 
 
 def _last_contiguous(g):
     """A gradient in the layout the library reads: an expanded or transposed one is copied."""
-    ok = g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(s % 8 == 0 and s > 0 for s in g.stride()[:-1])
-    return g if ok and (g.dim() < 3 or g.stride(0) >= g.shape[1] * g.stride(1)) else g.contiguous()
+    if g.is_contiguous() and g.data_ptr() % 16 == 0:
+        return g
+    st = g.stride()
+    ok = g.data_ptr() % 16 == 0 and st[-1] == 1 and all(s % 8 == 0 and s > 0 for s in st[:-1]) and (
+        st[-2] >= g.shape[-1]) and (g.dim() < 3 or st[0] >= g.shape[1] * st[1])
+    return g if ok else g.clone(memory_format=torch.contiguous_format)
 
 
 def rms_norm_fake_quant_ste(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,

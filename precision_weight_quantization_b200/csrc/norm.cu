@@ -289,6 +289,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(c
 // result does not depend on timing.  FP32 throughout: the inputs are BF16
 // and no value decides a code.
 
+// A CTA has `groups` groups of `tpr` threads, each group a row at a time.
+// Rows come in through shared memory by bulk copies, `ring` rows ahead: the
+// reduction's barrier, which every row has to wait for, would otherwise
+// empty the memory pipe (with one row ahead in registers the kernel ran at
+// two thirds of the copy rate at 8192 x 2560).
+
 struct NormBwdArgs {
     View dy, dh, h, dx;          // dh.ptr null: no gradient of h
     const uint4* weight;
@@ -297,63 +303,100 @@ struct NormBwdArgs {
     FastDiv rows;
     uint32_t total_rows;
     int vecs;
+    int groups, tpr, ring;
 };
+
+__device__ uint32_t g_norm_error = 0u;
+constexpr uint64_t kNormWaitNs = 2000000000ull;
+constexpr int kMaxRing = 4, kMaxGroups = 8;
 
 __device__ __forceinline__ float warp_sum_f(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
 
-// The next row's loads are in flight while this row is reduced and written.
-template <int kVec, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+//
+// kHoldW: the weight stays in registers (128 a thread up to 512 threads);
+// wider rows read it again from L1, so that 1024 threads do not spill.
+template <int kVec, int kMaxThreads, int kMinCtas, bool kHoldW>
+__global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+    extern __shared__ __align__(128) uint8_t smem_rows[];
     __shared__ float part[2][kMaxThreads / 32];
-    const int threads = (int)blockDim.x, step = 16 * threads;
+    __shared__ __align__(8) uint64_t bars[kMaxGroups * kMaxRing];
+    const int tpr = a.tpr, group = (int)threadIdx.x / tpr, t = (int)threadIdx.x - group * tpr;
+    const int warps = tpr / 32, warp0 = group * warps;
+    const uint32_t row_bytes = (uint32_t)a.vecs * 16u, stage = 3u * row_bytes;
+    const uint32_t ring = smem_addr(smem_rows) + (uint32_t)(group * a.ring) * stage;
+    const uint32_t full = smem_addr(bars) + 8u * (uint32_t)(group * kMaxRing);
     const bool has_dh = a.dh.ptr != nullptr;
+    const uint32_t bytes = has_dh ? stage : 2u * row_bytes;
     const float inv_d = __fdiv_rn(1.0f, (float)(8 * a.vecs));
+    const uint32_t first = blockIdx.x * (uint32_t)a.groups + (uint32_t)group, stride = gridDim.x * (uint32_t)a.groups;
+
+    if (t == 0) {
+        for (int i = 0; i < a.ring; ++i) mbar_init(full + 8u * i, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const uint64_t pol = l2_policy_evict_first();
+    auto fetch = [&](uint32_t r, uint32_t st) {   // one thread of the group
+        const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
+        const uint32_t at = ring + st * stage, bar = full + 8u * st;
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_load(at, a.dy.ptr + (int64_t)b * a.dy.bstride + (int64_t)m * a.dy.rstride, row_bytes, bar, pol);
+        bulk_load(at + row_bytes, a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride, row_bytes, bar, pol);
+        if (has_dh)
+            bulk_load(at + 2u * row_bytes, a.dh.ptr + (int64_t)b * a.dh.bstride + (int64_t)m * a.dh.rstride, row_bytes,
+                      bar, pol);
+    };
+    if (t == 0)
+        for (int i = 0; i < a.ring; ++i)
+            if ((uint64_t)first + (uint64_t)i * stride < a.total_rows) fetch(first + (uint32_t)i * stride, (uint32_t)i);
+
     float dw[kVec][8];
-    uint4 wv[kVec];
+    uint4 held[kHoldW ? kVec : 1];
+    auto weight = [&](int i) {
+        const int k = i * tpr + t;
+        return k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
+    };
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const int k = i * threads + (int)threadIdx.x;
-        wv[i] = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
+        if (kHoldW) held[i] = weight(i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     }
-    uint4 ng[kVec], nh[kVec], nd[kVec];
-    float nr = 0.0f;
-    auto fetch = [&](uint32_t r) {
-        const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
-        const char* dy = a.dy.ptr + (int64_t)b * a.dy.bstride + (int64_t)m * a.dy.rstride + 16 * threadIdx.x;
-        const char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride + 16 * threadIdx.x;
-        const char* dh = a.dh.ptr + (int64_t)b * a.dh.bstride + (int64_t)m * a.dh.rstride + 16 * threadIdx.x;
-        nr = __ldg(a.rstd + r);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const bool on = i * threads + (int)threadIdx.x < a.vecs;
-            ng[i] = on ? ld_stream_v4(dy + i * step) : make_uint4(0u, 0u, 0u, 0u);
-            nh[i] = on ? ld_stream_v4(h + i * step) : make_uint4(0u, 0u, 0u, 0u);
-            nd[i] = on && has_dh ? ld_stream_v4(dh + i * step) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    if (blockIdx.x < a.total_rows) fetch(blockIdx.x);
+    uint32_t st = 0u, phase = 0u;
     int flip = 0;
-    for (uint32_t r = blockIdx.x; r < a.total_rows; r += gridDim.x, flip ^= 1) {
+    bool alive = true;
+    for (uint64_t r64 = first; r64 < a.total_rows; r64 += stride, flip ^= 1) {
+        const uint32_t r = (uint32_t)r64;
+        const float rstd = __ldg(a.rstd + r);
+        if (alive && !mbar_wait_bounded(full + 8u * st, phase, kNormWaitNs)) {
+            atomicOr(&g_norm_error, kErrTmaTimeout);
+            alive = false;   // the outputs are unspecified from here; no further wait
+        }
         uint4 vg[kVec], vh[kVec], vd[kVec];
-        const float rstd = nr;
+        const uint32_t at = ring + st * stage + 16u * (uint32_t)t;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            vg[i] = ng[i];
-            vh[i] = nh[i];
-            vd[i] = nd[i];
+            const bool on = i * tpr + t < a.vecs;
+            const uint32_t o = at + 16u * (uint32_t)(i * tpr);
+            vg[i] = on ? ld_shared_v4(o) : make_uint4(0u, 0u, 0u, 0u);
+            vh[i] = on ? ld_shared_v4(o + row_bytes) : make_uint4(0u, 0u, 0u, 0u);
+            vd[i] = on && has_dh ? ld_shared_v4(o + 2u * row_bytes) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (r + gridDim.x < a.total_rows) fetch(r + gridDim.x);
         float c = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
-            const uint32_t w[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+            const uint4 wv = kHoldW ? held[kHoldW ? i : 0] : weight(i);
+            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float t0 = bf16_lo(g[j]) * (bf16_lo(hh[j]) * rstd), t1 = bf16_hi(g[j]) * (bf16_hi(hh[j]) * rstd);
@@ -364,20 +407,29 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
             }
         }
         c = warp_sum_f(c);
-        if (threads > 32) {
-            if ((threadIdx.x & 31) == 0) part[flip][threadIdx.x >> 5] = c;
-            __syncthreads();   // one barrier a row: the two halves of `part` alternate
+        if ((t & 31) == 0) part[flip][warp0 + (t >> 5)] = c;
+        // every thread of the group has read the stage; the two halves of `part` alternate
+        if (warps > 1) asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "r"(tpr) : "memory");
+        else __syncwarp();
+        const uint64_t next = r64 + (uint64_t)a.ring * stride;
+        if (t == 0 && alive && next < a.total_rows) fetch((uint32_t)next, st);
+        if (++st == (uint32_t)a.ring) {
+            st = 0u;
+            phase ^= 1u;
+        }
+        if (warps > 1) {
             c = 0.0f;
-            for (int i = 0; i < threads / 32; ++i) c += part[flip][i];
+            for (int i = 0; i < warps; ++i) c += part[flip][warp0 + i];
         }
         c *= inv_d;
         const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
-        char* dx = a.dx.ptr + (int64_t)b * a.dx.bstride + (int64_t)m * a.dx.rstride + 16 * threadIdx.x;
+        char* dx = a.dx.ptr + (int64_t)b * a.dx.bstride + (int64_t)m * a.dx.rstride + 16 * t;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            if (i * threads + (int)threadIdx.x >= a.vecs) continue;
+            if (i * tpr + t >= a.vecs) continue;
             const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
-            const uint32_t w[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w}, d[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
+            const uint4 wv = kHoldW ? held[kHoldW ? i : 0] : weight(i);
+            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w}, d[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -385,40 +437,57 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
                 const float e1 = __fmaf_rn(bf16_hi(hh[j]) * rstd, -c, bf16_hi(g[j]) * bf16_hi(w[j]));
                 o[j] = pack_bf16x2(__fmaf_rn(e0, rstd, bf16_lo(d[j])), __fmaf_rn(e1, rstd, bf16_hi(d[j])));
             }
-            st_v4(dx + i * step, make_uint4(o[0], o[1], o[2], o[3]));
+            st_v4(dx + (int64_t)16 * (i * tpr), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
-    if (a.parts) {
-        float* p = a.parts + (int64_t)blockIdx.x * a.vecs * 8;
+    if (!a.parts) return;
+    // the groups' dweights are added in group order in shared memory (every row's copy has been read)
+    float* sum = reinterpret_cast<float*>(smem_rows);
+    for (int g = 0; g < a.groups; ++g) {
+        __syncthreads();
+        if (group != g) continue;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int k = i * threads + (int)threadIdx.x;
+            const int k = i * tpr + t;
             if (k >= a.vecs) continue;
-            float* q = p + 8 * (int64_t)k;
-            st_v4(q, make_uint4(__float_as_uint(dw[i][0]), __float_as_uint(dw[i][1]), __float_as_uint(dw[i][2]),
-                                __float_as_uint(dw[i][3])));
-            st_v4(q + 4, make_uint4(__float_as_uint(dw[i][4]), __float_as_uint(dw[i][5]), __float_as_uint(dw[i][6]),
-                                    __float_as_uint(dw[i][7])));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (g > 0) dw[i][j] += sum[8 * k + j];
+                if (g < a.groups - 1) sum[8 * k + j] = dw[i][j];
+            }
+            if (g == a.groups - 1) {
+                float* q = a.parts + (int64_t)blockIdx.x * a.vecs * 8 + 8 * (int64_t)k;
+                st_v4(q, make_uint4(__float_as_uint(dw[i][0]), __float_as_uint(dw[i][1]), __float_as_uint(dw[i][2]),
+                                    __float_as_uint(dw[i][3])));
+                st_v4(q + 4, make_uint4(__float_as_uint(dw[i][4]), __float_as_uint(dw[i][5]), __float_as_uint(dw[i][6]),
+                                        __float_as_uint(dw[i][7])));
+            }
         }
     }
 }
 
-// dweight[d] = sum of the parts in a fixed order: 8 warps take every eighth
-// part of 32 columns, then the 8 sums are added.
-__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* parts, int n_parts, int D, void* dweight,
-                                                           int bf16_out) {
-    __shared__ float s[8][32];
+// dweight[d] = sum of the parts in a fixed order: 32 warps take every 32nd
+// part of 32 columns, eight loads in flight each, then the 32 sums are added.
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* parts, int n_parts, int D, void* dweight,
+                                                            int bf16_out) {
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = (int)blockIdx.x * 32 + lane;
     float v = 0.0f;
-    if (d < D)
-        for (int p = warp; p < n_parts; p += 8) v += __ldg(parts + (int64_t)p * D + d);
+    for (int p = warp; p < n_parts; p += 8 * 32) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = d < D && p + 32 * i < n_parts ? __ldg(parts + (int64_t)(p + 32 * i) * D + d) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += t[i];
+    }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && d < D) {
         v = s[0][lane];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][lane];
+        for (int i = 1; i < 32; ++i) v += s[i][lane];
         if (bf16_out) static_cast<uint16_t*>(dweight)[d] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
         else static_cast<float*>(dweight)[d] = v;
     }
@@ -444,12 +513,26 @@ cudaError_t launch_norm_kind(const NormArgs& a, cudaStream_t s) {
     return launch_norm_out<kOut, 4, 1024>(a, norm_threads(D, 4), s);
 }
 
-// Vectors per thread of the backward pass: two while a CTA's threads hold the row.
-int norm_bwd_vec(int64_t D) { return D <= 16384 ? 2 : 4; }
-
-int norm_bwd_grid(int64_t rows, int64_t D) {
-    const int threads = norm_threads(D, norm_bwd_vec(D));
-    return persistent_grid(rows, std::max(1, std::min(16, 640 / threads)));
+// Launch shape of the backward pass: two vectors per thread while 1024 threads
+// hold the row, four above; small rows share a CTA of about 256 threads (one
+// dweight part per CTA), and as many rows ahead as shared memory holds.
+struct BwdShape {
+    int vec, tpr, groups, ctas, ring, grid;
+    size_t smem;
+};
+constexpr size_t kBwdSmem = 200 * 1024;   // per SM
+BwdShape norm_bwd_shape(int64_t rows, int64_t D) {
+    BwdShape s;
+    s.vec = D <= 16384 ? 2 : 4;
+    s.tpr = norm_threads(D, s.vec);
+    s.groups = std::max(1, std::min(kMaxGroups, 256 / s.tpr));
+    const int threads = s.tpr * s.groups;
+    s.ctas = std::max(1, 512 / threads);   // 128 registers a thread
+    const size_t stage = 6 * (size_t)D * s.groups;
+    s.ring = (int)std::max<size_t>(1, std::min<size_t>(kMaxRing, kBwdSmem / s.ctas / stage));
+    s.smem = s.ring * stage;
+    s.grid = persistent_grid((rows + s.groups - 1) / s.groups, s.ctas);
+    return s;
 }
 
 }  // namespace
@@ -481,7 +564,28 @@ cudaError_t launch_norm(const Norm& n, cudaStream_t s) {
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
-    return ((size_t)norm_bwd_grid(rows, D) * (size_t)D * 4 + 255) / 256 * 256;
+    return ((size_t)norm_bwd_shape(rows, D).grid * (size_t)D * 4 + 255) / 256 * 256;
+}
+
+namespace {
+
+template <int kVec, int kMaxThreads, int kMinCtas, bool kHoldW>
+cudaError_t launch_bwd_kernel(const NormBwdArgs& a, const BwdShape& sh, cudaStream_t s) {
+    static int configured[kMaxDevices] = {0};
+    const void* fn = (const void*)norm_bwd_kernel<kVec, kMaxThreads, kMinCtas, kHoldW>;
+    const cudaError_t e = set_smem_limit_once(configured, &fn, 1, (int)kBwdSmem);
+    if (e != cudaSuccess) return e;
+    norm_bwd_kernel<kVec, kMaxThreads, kMinCtas, kHoldW><<<sh.grid, sh.tpr * sh.groups, sh.smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_norm_error(uint32_t* code) {
+    uint32_t zero = 0u;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_norm_error, sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_norm_error, &zero, sizeof(uint32_t));
 }
 
 cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
@@ -496,16 +600,18 @@ cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
     a.rows = make_fastdiv((uint32_t)n.h.rows);
     a.total_rows = (uint32_t)(n.h.batch * n.h.rows);
     a.vecs = (int)(n.h.cols / 8);
-    const int64_t cols = n.h.cols;
-    const int vec = norm_bwd_vec(cols), threads = norm_threads(cols, vec), grid = norm_bwd_grid(a.total_rows, cols);
-    if (vec == 2 && threads <= 256) norm_bwd_kernel<2, 256><<<grid, threads, 0, s>>>(a);
-    else if (vec == 2 && threads <= 512) norm_bwd_kernel<2, 512><<<grid, threads, 0, s>>>(a);
-    else if (vec == 2) norm_bwd_kernel<2, 1024><<<grid, threads, 0, s>>>(a);
-    else norm_bwd_kernel<4, 1024><<<grid, threads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const BwdShape sh = norm_bwd_shape(a.total_rows, n.h.cols);
+    a.groups = sh.groups;
+    a.tpr = sh.tpr;
+    a.ring = sh.ring;
+    const int threads = sh.tpr * sh.groups;
+    const cudaError_t e = sh.vec == 4       ? launch_bwd_kernel<4, 1024, 1, false>(a, sh, s)
+                          : threads <= 256 ? launch_bwd_kernel<2, 256, 2, true>(a, sh, s)
+                          : threads <= 512 ? launch_bwd_kernel<2, 512, 1, true>(a, sh, s)
+                                           : launch_bwd_kernel<2, 1024, 1, false>(a, sh, s);
     if (e != cudaSuccess || !n.dweight) return e;
     const int D = (int)n.h.cols;
-    norm_dweight_kernel<<<(D + 31) / 32, 256, 0, s>>>(a.parts, grid, D, n.dweight, n.dweight_bf16);
+    norm_dweight_kernel<<<(D + 31) / 32, 1024, 0, s>>>(a.parts, sh.grid, D, n.dweight, n.dweight_bf16);
     return cudaGetLastError();
 }
 

@@ -288,7 +288,10 @@ pwq_status pwq_device_error(uint32_t* code) {
     uint32_t c = 0;
     e = pwq::read_and_clear_matmul_error(&c);
     if (e != cudaSuccess) return cuda_fail(e);
-    *code = a | b | c;
+    uint32_t d = 0;
+    e = pwq::read_and_clear_norm_error(&d);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *code = a | b | c | d;
     return PWQ_OK;
 }
 

@@ -208,6 +208,7 @@ struct NormBwd {
 };
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t D);
 cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s);
+cudaError_t read_and_clear_norm_error(uint32_t* code);
 
 cudaError_t launch_selftest_division(int which, unsigned long long* counts, cudaStream_t s);
 cudaError_t launch_selftest_codecs(uint32_t first, uint32_t count, uint8_t* e4m3, uint8_t* e2m1,

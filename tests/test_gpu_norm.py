@@ -418,3 +418,11 @@ def test_refusals(P):
     buf = torch.zeros(8, 64, dtype=torch.bfloat16, device=DEV)
     assert status(lambda: P.rms_norm_mxfp8(buf[:4], w, buf[4:], h=buf[2:6])) == "PWQ_ERR_OVERLAP"
     assert status(lambda: P.rms_norm_backward(x, x, w, torch.ones(4, device=DEV), out=x)) == "PWQ_ERR_OVERLAP"
+
+
+def test_second_derivative_is_refused(P):
+    x, w, r = (t.to(DEV) for t in inputs((4, 64), 96))
+    leaf = x.detach().requires_grad_()
+    y, h = P.rms_norm_fake_quant_ste(leaf, w, r)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y.float().square().sum(), leaf, create_graph=True)
