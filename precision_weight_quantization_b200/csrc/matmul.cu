@@ -83,7 +83,7 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 //
 // Warps 0..3 epilogue, 4 TMA producer, 5 MMA issuer and TMEM owner.
 
-constexpr int kTokThreads = 192;
+constexpr int kTokThreads = 192, kMaxSplit = 8;
 
 struct TokArgs {
     CUtensorMap w, ws, t, ts;    // weight codes / scales, token codes / scales
@@ -95,6 +95,7 @@ struct TokArgs {
     int w_bands, t_bands;        // 128-row scale bands per batch slab
     int steps, last_mmas;        // 128-byte steps of K, MMAs of the last one
     int split;                   // CTAs per cluster along K
+    int y8;                      // y rows are 8-byte aligned
     FastDiv w_tiles, t_tiles;
 };
 
@@ -103,7 +104,8 @@ struct TokCfg {
     using T = ProductTraits<kF>;
     static constexpr uint32_t kW = 128u * kStepBytes, kT = (uint32_t)kTok * kStepBytes;
     static constexpr uint32_t kStage = kW + kT + 2u * T::kScaleBytes;
-    static constexpr int kStages = kTok <= 64 ? 4 : 3;
+    // two CTAs per SM: a tile more than there are SMs must not cost a second wave
+    static constexpr int kStages = (kTok <= 32 || (kTok == 64 && !T::kFp4)) ? 4 : 3;
     static constexpr uint32_t kSmem = kStages * kStage + 1024u;   // + alignment of the ring to 1024 bytes
     // TMEM: kTok accumulator columns, then two buffers of weight and token scale columns
     static constexpr uint32_t kScaleCols = 4u * T::kScaleTiles;
@@ -236,14 +238,37 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
         __syncwarp();
         cluster_sync();
         if (warp < 4) {
+            // this CTA finishes tokens rank, rank + split, ...; a warp takes one at a time, a lane four weight
+            // rows, and the partials of all CTAs are loaded before the first addition (a load from a
+            // neighbour takes several hundred clocks)
             const float2 sc = output_scale(a.gt, a.gw, b);
-            const int n = n0 + (int)threadIdx.x;
-            uint16_t* y = a.y + (int64_t)b * a.y_bs + n;
-            for (int c = (int)rank; c < kTok && t0 + c < a.m; c += a.split) {
-                float sum = 0.0f;
-                for (int q = 0; q < a.split; ++q)
-                    sum += ld_cluster_f32(cluster_addr(ring + ((uint32_t)c * 128u + threadIdx.x) * 4u, (uint32_t)q));
-                if (n < a.n) y[(int64_t)(t0 + c) * a.y_rs] = bf16_bits(sum * sc.x * sc.y);
+            const int n = n0 + lane * 4;
+            for (int c = (int)rank + warp * a.split; c < kTok && t0 + c < a.m; c += 4 * a.split) {
+                const uint32_t at = ring + (uint32_t)c * 512u + (uint32_t)lane * 16u;
+                float4 v[kMaxSplit];
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q)
+                    if (q < a.split) v[q] = ld_cluster_v4(cluster_addr(at, (uint32_t)q));
+                float4 s = v[0];
+#pragma unroll
+                for (int q = 1; q < kMaxSplit; ++q)
+                    if (q < a.split) {
+                        s.x += v[q].x;
+                        s.y += v[q].y;
+                        s.z += v[q].z;
+                        s.w += v[q].w;
+                    }
+                const uint2 o = make_uint2(pack_bf16x2(s.x * sc.x * sc.y, s.y * sc.x * sc.y),
+                                           pack_bf16x2(s.z * sc.x * sc.y, s.w * sc.x * sc.y));
+                uint16_t* y = a.y + (int64_t)b * a.y_bs + (int64_t)(t0 + c) * a.y_rs + n;
+                if (a.y8 && n + 4 <= a.n) {
+                    st_v2(y, o);
+                } else {
+                    if (n < a.n) y[0] = (uint16_t)o.x;
+                    if (n + 1 < a.n) y[1] = (uint16_t)(o.x >> 16);
+                    if (n + 2 < a.n) y[2] = (uint16_t)o.y;
+                    if (n + 3 < a.n) y[3] = (uint16_t)(o.y >> 16);
+                }
             }
         }
         __syncwarp();
@@ -596,6 +621,7 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
     a.y = reinterpret_cast<uint16_t*>(p.y.ptr);
     a.y_bs = p.y.bstride / 2;
     a.y_rs = p.y.rstride / 2;
+    a.y8 = (uintptr_t)p.y.ptr % 8 == 0 && p.y.rstride % 8 == 0 && (p.y.batch == 1 || p.y.bstride % 8 == 0);
     a.n = (int)p.w.rows;
     a.m = (int)p.a.rows;
     a.steps = (int)((row_bytes + kStepBytes - 1) / kStepBytes);
@@ -605,7 +631,7 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
     // split K while the tiles leave half of the resident CTA slots (two per SM) empty
     const int64_t slots = 2 * (int64_t)sm_count(current_device());
     a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= slots && a.split * 2 <= a.steps) a.split *= 2;
+    while (a.split < kMaxSplit && tiles * a.split * 2 <= slots && a.split * 2 <= a.steps) a.split *= 2;
     if (tiles * a.split > (int64_t)0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * a.split));
