@@ -37,6 +37,7 @@ __device__ __forceinline__ bool wait_or_record(uint32_t bar, uint32_t parity) {
 }
 
 // The same for a converged warp: every lane waits, and all get one answer.
+// (One lane that polls for the warp takes 200 clocks longer to get through.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_or_record(bar, parity));
 }
@@ -81,9 +82,9 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 // FP32 partials meet in distributed shared memory and are added in rank
 // order (the result does not depend on timing).
 //
-// Warps 0..3 epilogue, 4 TMA producer, 5 MMA issuer and TMEM owner.
+// Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales), 5 MMA issuer and TMEM owner.
 
-constexpr int kTokThreads = 192, kMaxSplit = 8;
+constexpr int kTokThreads = 224, kMaxSplit = 8;
 
 struct TokArgs {
     CUtensorMap w, ws, t, ts;    // weight codes / scales, token codes / scales
@@ -105,12 +106,12 @@ struct TokCfg {
     static constexpr uint32_t kW = 128u * kStepBytes, kT = (uint32_t)kTok * kStepBytes;
     static constexpr uint32_t kStage = kW + kT + 2u * T::kScaleBytes;
     // two CTAs per SM: a tile more than there are SMs must not cost a second wave
-    static constexpr int kStages = (kTok <= 32 || (kTok == 64 && !T::kFp4)) ? 4 : 3;
+    static constexpr int kStages = kTok <= 16 || (kTok == 32 && !T::kFp4) ? 5 : kTok == 32 || (kTok == 64 && !T::kFp4) ? 4 : 3;
     static constexpr uint32_t kSmem = kStages * kStage + 1024u;   // + alignment of the ring to 1024 bytes
-    // TMEM: kTok accumulator columns, then two buffers of weight and token scale columns
+    // TMEM: kTok accumulator columns, then a buffer of weight and token scale columns for each stage
     static constexpr uint32_t kScaleCols = 4u * T::kScaleTiles;
-    static constexpr uint32_t kCols = kTok + 4u * kScaleCols <= 128u ? 128u : 256u;
-    static_assert(kTok + 4u * kScaleCols <= kCols, "TMEM");
+    static constexpr uint32_t kCols = 256u;   // two CTAs per SM fill it
+    static_assert(kTok + 2u * kStages * kScaleCols <= kCols, "TMEM");
     static_assert(128u * kTok * 4u <= kStages * kStage, "the FP32 partial reuses the ring");
 };
 
@@ -145,13 +146,21 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
         mbar_init(done, 1);
         fence_mbar_init();
     }
+    if (warp == 4 && elect_one()) {
+        prefetch_tensor_map(&a.w);
+        prefetch_tensor_map(&a.t);
+        prefetch_tensor_map(&a.ws);
+        prefetch_tensor_map(&a.ts);
+    }
     if (warp == 5) tmem_alloc<1>(smem_addr(&tmem_word), C::kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_word, 0);
 
-    if (warp == 4) {
+    if (warp == 4 || warp == 6) {
+        const bool codes = warp == 4;   // the other one loads the scales
+        const int w_band = b * a.w_bands + wt, t_band = b * a.t_bands + t0 / 128;
         int i = 0;
         for (; i < steps; ++i) {
             const int st = i % kS;
@@ -159,30 +168,34 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
             const uint32_t at = ring + (uint32_t)st * C::kStage, bar = full + 8u * st;
             const int s = s0 + i;
             if (elect_one()) {
-                mbar_arrive_expect_tx(bar, C::kStage);
-                tma_load_3d(at, &a.w, bar, s * (int)kStepBytes, n0, b);
-                tma_load_3d(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0, b);
-                tma_load_3d(at + C::kW + C::kT, &a.ws, bar, 0, s * T::kScaleTiles, b * a.w_bands + wt);
-                tma_load_3d(at + C::kW + C::kT + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
-                            b * a.t_bands + t0 / 128);
+                if (codes) {
+                    mbar_arrive_expect_tx(bar, C::kStage);
+                    tma_load_3d(at, &a.w, bar, s * (int)kStepBytes, n0, b);
+                    tma_load_3d(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0, b);
+                } else {
+                    tma_load_3d(at + C::kW + C::kT, &a.ws, bar, 0, s * T::kScaleTiles, w_band);
+                    tma_load_3d(at + C::kW + C::kT + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles, t_band);
+                }
             }
             __syncwarp();
         }
         // no copy is in flight when the CTA ends
-        for (int j = max(0, i - kS); j < i; ++j) warp_wait(full + 8u * (j % kS), (j / kS) & 1);
+        if (codes)
+            for (int j = max(0, i - kS); j < i; ++j)
+                if (!warp_wait(full + 8u * (j % kS), (j / kS) & 1)) break;
     } else if (warp == 5) {
         constexpr uint32_t idesc = mma_idesc<kF>(128, kTok);
+        const bool leader = elect_one();
+        bool ready = false;   // the next operands' barrier, tested while a step is issued
         for (int i = 0; i < steps; ++i) {
-            const int st = i % kS;
-            if (!warp_wait(full + 8u * st, (i / kS) & 1)) break;
-            // the scale columns of step i - 2 are read no more
-            if (i >= 2 && !warp_wait(empty + 8u * ((i - 2) % kS), ((i - 2) / kS) & 1)) break;
+            const int st = i % kS, nx = (i + 1) % kS;
+            if (!__all_sync(0xffffffffu, ready) && !warp_wait(full + 8u * st, (i / kS) & 1)) break;
             tc_fence_after();
             const uint32_t at = ring + (uint32_t)st * C::kStage;
-            const uint32_t sw = tmem + kTok + (uint32_t)(i & 1) * 2u * C::kScaleCols, sx = sw + C::kScaleCols;
+            const uint32_t sw = tmem + kTok + (uint32_t)st * 2u * C::kScaleCols, sx = sw + C::kScaleCols;
             const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
             const int mmas = s0 + i == a.steps - 1 ? a.last_mmas : kMmasPerStep;
-            if (elect_one()) {
+            if (leader) {
 #pragma unroll
                 for (int j = 0; j < T::kScaleTiles; ++j) {
                     copy_scales<1>(sw + 4u * j, desc_scales(at + C::kW + C::kT + 512u * j));
@@ -195,14 +208,15 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
                     const uint32_t so = T::kFp4 ? 4u * j : 0u;
                     mma_block_scaled<kF, 1>(tmem, dw + 2u * j, dx + 2u * j, id, sw + so, sx + so, (i | j) != 0);
                 }
-                mma_commit(empty + 8u * st);
             }
-            __syncwarp();
+            ready = mbar_test(full + 8u * nx, ((i + 1) / kS) & 1);
+            if (leader) mma_commit(empty + 8u * st);
         }
+        __syncwarp();
         if (elect_one()) mma_commit(done);
         __syncwarp();
     } else {
-        const bool ok = wait_or_record(done, 0);
+        const bool ok = vote_all(warp != 0 || warp_wait(done, 0));   // the first warp polls for the four
         tc_fence_after();
         const float2 sc = output_scale(a.gt, a.gw, b);
         const int n = n0 + warp * 32 + lane;
@@ -304,9 +318,10 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // starts at a multiple of 64 rows of a 128-row band (and its scales span at
 // most two bands).  The host picks the one with the least work in the last wave.
 //
-// Warps 0..3 epilogue, 4 TMA producer, 5 MMA issuer (first CTA) and TMEM owner.
+// Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales: one warp issuing
+// all four loads took 0.31 us per step), 5 MMA issuer (first CTA) and TMEM owner.
 
-constexpr int kPairThreads = 192;
+constexpr int kPairThreads = 224;
 constexpr uint32_t kGroup = 8;
 constexpr int kOutTokens = 32;                                    // tokens per output store
 constexpr uint32_t kOutBytes = 64u * kOutTokens * 2u;             // 64 weight rows x 32 tokens, BF16
@@ -322,26 +337,23 @@ struct PairArgs {
     int w_bands, t_bands;
     int steps, last_mmas;
     int tile_t, t_band_box;      // tokens per tile, scale bands per tile
+    uint32_t stages, stage, scale_stage, out_at, scales_at;   // ring: stages, bytes of codes and of scales per stage
+    uint32_t scale_bufs;         // scale buffers in TMEM
     uint32_t w_tiles, t_tiles, tiles;
     FastDiv per_batch, per_group;   // w_tiles * t_tiles, w_tiles * kGroup
 };
 
+constexpr int kMaxStages = 12;
+constexpr uint32_t kPairSmem = 232448u - 512u;   // dynamic shared memory of a CTA (the rest is static)
+
 template <ProductFormat kF>
 struct PairCfg {
     using T = ProductTraits<kF>;
-    static constexpr uint32_t kW = 128u * kStepBytes, kT = 128u * kStepBytes;
-    static constexpr uint32_t kStage = kW + kT;                               // codes
-    static constexpr uint32_t kScales = 3u * T::kScaleBytes;                  // one band of weights, two of tokens
-    static constexpr int kStages = T::kFp4 ? 5 : 6;
+    static constexpr uint32_t kW = 128u * kStepBytes;
     static constexpr uint32_t kOutBufs = T::kFp4 ? 4u : 3u;                   // output staging buffers per warp pair
-    static constexpr uint32_t kOutAt = kStages * kStage, kScalesAt = kOutAt + 2u * kOutBufs * kOutBytes;
-    static constexpr uint32_t kSmem = kScalesAt + kStages * kScales + 1024u;
-    static constexpr uint32_t kScaleBufs = T::kFp4 ? 3u : 5u;
     static constexpr uint32_t kScaleCols = 12u * T::kScaleTiles;              // per buffer: 4 weights + 8 tokens per tile
-    static constexpr uint32_t kScaleAt = 512u - kScaleBufs * kScaleCols;
-    static constexpr int kMaxShared = (512 - (int)kScaleAt / 32 * 32) / 32;   // 32-column chunks in both accumulators
-    static_assert(kScaleBufs < kStages, "a scale buffer's last step still owns its barrier phase");
-    static_assert(kSmem <= 232448u - 256u, "shared memory");
+    // 32-column chunks that two accumulators of 256 columns share: with three buffers of 48 / six of 12
+    static constexpr int kMaxShared = T::kFp4 ? 5 : 3;
 };
 
 struct PairTile {
@@ -365,22 +377,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ PairArgs a) {
     using T = ProductTraits<kF>;
     using C = PairCfg<kF>;
-    constexpr int kS = C::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kS + 4];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
     __shared__ uint32_t tmem_word;
-    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, scales = ring + C::kScalesAt;
-    const uint32_t full = smem_addr(bars), empty = full + 8u * kS;
-    const uint32_t acc_full = empty + 8u * kS, acc_free = acc_full + 16u;   // [2] each
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, scales = ring + a.scales_at;
+    const uint32_t full = smem_addr(bars), empty = full + 8u * kMaxStages;
+    const uint32_t acc_full = empty + 8u * kMaxStages, acc_free = acc_full + 16u;   // [2] each
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     // the second accumulator's column, and the 32-column chunks that the two share
-    const uint32_t acc1 = min((uint32_t)a.tile_t, (C::kScaleAt - (uint32_t)a.tile_t) / 32u * 32u);
+    const uint32_t scale_at = 512u - a.scale_bufs * C::kScaleCols;
+    const uint32_t acc1 = min((uint32_t)a.tile_t, (scale_at - (uint32_t)a.tile_t) / 32u * 32u);
     const int shared = (a.tile_t - (int)acc1) / 32;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kS; ++i) {
+        for (uint32_t i = 0; i < a.stages; ++i) {
             mbar_init(full + 8u * i, 1);
             mbar_init(empty + 8u * i, 1);
         }
@@ -390,6 +402,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         fence_mbar_init();
     }
+    if (warp == 4 && elect_one()) {
+        prefetch_tensor_map(&a.w);
+        prefetch_tensor_map(&a.t);
+        prefetch_tensor_map(&a.ws);
+        prefetch_tensor_map(&a.ts);
+    }
     if (warp == 5) tmem_alloc<2>(smem_addr(&tmem_word), 512);
     tc_fence_before();
     __syncthreads();
@@ -397,41 +415,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_word, 0);
 
-    if (warp == 4) {
+    if (warp == 4 || warp == 6) {
+        const bool codes = warp == 4;   // the other one loads the scales
         const uint32_t tok_bytes = (uint32_t)a.tile_t / 2u * kStepBytes;
         const uint32_t bytes = C::kW + tok_bytes + (1u + (uint32_t)a.t_band_box) * T::kScaleBytes;
-        uint32_t it = 0;
+        RingPos pos;
+        uint32_t issued = 0;
         bool ok = true;
         for (uint32_t i = first; ok && i < a.tiles; i += stride) {
             const PairTile p = pair_tile(a, i);
             const int wt = p.wt * 2 + (int)rank, t0 = p.tt * a.tile_t;
-            for (int s = 0; s < a.steps; ++s, ++it) {
-                const uint32_t st = it % kS;
-                if (it >= kS && !warp_wait(empty + 8u * st, (it / kS - 1u) & 1u)) {
+            const int w_band = p.b * a.w_bands + wt, t_band = p.b * a.t_bands + t0 / 128;
+            const int w_row = wt * 128, t_row = t0 + (int)rank * (a.tile_t / 2);
+            for (int s = 0; s < a.steps; ++s) {
+                const uint32_t st = pos.at, bar = cluster_addr(full + 8u * st, 0);
+                if (!warp_wait(empty + 8u * st, pos.phase ^ 1u)) {   // passes at once on the first lap
                     ok = false;
                     break;
                 }
-                const uint32_t at = ring + st * C::kStage, bar = cluster_addr(full + 8u * st, 0);
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8u * st, 2u * bytes);
-                    tma_load_3d_pair(at, &a.w, bar, s * (int)kStepBytes, wt * 128, p.b);
-                    tma_load_3d_pair(at + C::kW, &a.t, bar, s * (int)kStepBytes, t0 + (int)rank * (a.tile_t / 2), p.b);
-                    const uint32_t sc = scales + st * C::kScales;
-                    tma_load_3d_pair(sc, &a.ws, bar, 0, s * T::kScaleTiles, p.b * a.w_bands + wt);
-                    tma_load_3d_pair(sc + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles,
-                                     p.b * a.t_bands + t0 / 128);
+                    if (codes) {
+                        const uint32_t at = ring + st * a.stage;
+                        if (rank == 0) mbar_arrive_expect_tx(full + 8u * st, 2u * bytes);
+                        tma_load_3d_pair(at, &a.w, bar, s * (int)kStepBytes, w_row, p.b);
+                        tma_load_3d_pair(at + C::kW, &a.t, bar, s * (int)kStepBytes, t_row, p.b);
+                    } else {
+                        const uint32_t sc = scales + st * a.scale_stage;
+                        tma_load_3d_pair(sc, &a.ws, bar, 0, s * T::kScaleTiles, w_band);
+                        tma_load_3d_pair(sc + T::kScaleBytes, &a.ts, bar, 0, s * T::kScaleTiles, t_band);
+                    }
                 }
                 __syncwarp();
+                pos.next(a.stages);
+                ++issued;
             }
         }
-        // no copy of either CTA is in flight when the pair ends
-        if (rank == 0)
-            for (uint32_t j = it > kS ? it - kS : 0u; j < it; ++j) warp_wait(full + 8u * (j % kS), (j / kS) & 1u);
+        // no copy of either CTA is in flight when the pair ends: the stages' last uses, oldest first
+        if (rank == 0 && codes) {
+            const uint32_t end = pos.at;
+            for (uint32_t j = 0; j < a.stages; ++j) {
+                const bool last_lap = j < a.stages - end;   // used on the lap before, if there was one
+                if ((!last_lap || issued >= a.stages) && !warp_wait(full + 8u * pos.at, pos.phase ^ 1u)) break;
+                pos.next(a.stages);
+            }
+        }
     } else if (warp == 5) {
         if (rank == 0) {
             const uint32_t idesc = mma_idesc<kF>(256, a.tile_t);
-            uint32_t it = 0, n = 0;
-            bool ok = true;
+            // NVFP4: three scale buffers, each free again when the step three before has ended (`old`).  MXFP8: a
+            // buffer for each stage, free with it.
+            RingPos pos, old;
+            uint32_t it = 0, n = 0, sbuf = 0;
+            bool ok = true, ready = false;
+            const bool leader = elect_one();
             for (uint32_t i = first; ok && i < a.tiles; i += stride, ++n) {
                 const PairTile p = pair_tile(a, i);
                 const uint32_t buf = n & 1u, acc = tmem + buf * acc1;
@@ -441,22 +477,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (shared > 0 && n >= 1) ok = warp_wait(acc_free + 8u * (buf ^ 1u), ((n - 1u) / 2u) & 1u);
                 if (shared == 0 && n >= 2) ok = warp_wait(acc_free + 8u * buf, (n / 2u - 1u) & 1u);
                 if (!ok) break;
-                tc_fence_after();
-                for (int s = 0; s < a.steps; ++s, ++it) {
-                    const uint32_t st = it % kS;
-                    if (!warp_wait(full + 8u * st, (it / kS) & 1u) ||
-                        // the scale buffer's last step has ended
-                        (it >= C::kScaleBufs && !warp_wait(empty + 8u * ((it - C::kScaleBufs) % kS),
-                                                           ((it - C::kScaleBufs) / kS) & 1u))) {
-                        ok = false;
-                        break;
+                for (int s = 0; s < a.steps; ++s) {
+                    const uint32_t st = pos.at;
+                    // `ready`: the barriers were tested while the last step was issued
+                    if (!__all_sync(0xffffffffu, ready)) {
+                        ok = warp_wait(full + 8u * st, pos.phase);
+                        if (T::kFp4 && ok && it >= 3u) ok = warp_wait(empty + 8u * old.at, old.phase);
+                        if (!ok) break;
                     }
+                    if (T::kFp4 && it >= 3u) old.next(a.stages);
                     tc_fence_after();
-                    const uint32_t at = ring + st * C::kStage, sc = scales + st * C::kScales;
-                    const uint32_t sw = tmem + C::kScaleAt + it % C::kScaleBufs * C::kScaleCols;
+                    const uint32_t at = ring + st * a.stage, sc = scales + st * a.scale_stage;
+                    const uint32_t sw = tmem + scale_at + (T::kFp4 ? sbuf : st) * C::kScaleCols;
                     const uint64_t dw = desc_swizzle128(at), dx = desc_swizzle128(at + C::kW);
                     const int mmas = s == a.steps - 1 ? a.last_mmas : kMmasPerStep;
-                    if (elect_one()) {
+                    if (leader) {
 #pragma unroll
                         for (int j = 0; j < kMmasPerStep; ++j) {
                             if (j >= mmas) break;
@@ -471,9 +506,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
                             mma_block_scaled<kF, 2>(acc, dw + 2u * j, dx + 2u * j, id, cw, cx + tok_col, (s | j) != 0);
                         }
-                        mma_commit_pair(empty + 8u * st);
                     }
-                    __syncwarp();
+                    ++it;
+                    if (++sbuf == 3u) sbuf = 0u;
+                    pos.next(a.stages);
+                    const bool operands = mbar_test(full + 8u * pos.at, pos.phase);
+                    const bool buffer = !T::kFp4 || it < 3u || mbar_test(empty + 8u * old.at, old.phase);
+                    if (leader) mma_commit_pair(empty + 8u * st);
+                    ready = operands && buffer;
                 }
                 if (elect_one()) mma_commit_pair(acc_full + 8u * buf);
                 __syncwarp();
@@ -482,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else {
         uint32_t n = 0, stores = 0;
         const uint32_t row = tmem + ((uint32_t)warp << 21);
-        const uint32_t out = ring + C::kOutAt + (uint32_t)(warp >> 1) * C::kOutBufs * kOutBytes;
+        const uint32_t out = ring + a.out_at + (uint32_t)(warp >> 1) * C::kOutBufs * kOutBytes;
         // this lane's stmatrix row: token lane % 8 of eight, weight rows 8 (lane / 8) .. + 7 of the warp's 32
         const uint32_t c8 = (uint32_t)lane & 7u;
         const uint32_t frag = c8 * 128u + (((uint32_t)(warp & 1) * 4u + ((uint32_t)lane >> 3)) ^ c8) * 16u;
@@ -542,7 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         if (t + c < a.m) yp[(int64_t)(t + c) * a.y_rs] = bf16_bits(scaled<kF>(v[c], sc));
                 }
             };
-            if (!vote_all(wait_or_record(acc_full + 8u * buf, (n / 2u) & 1u))) break;   // the four warps leave together
+            // the first warp polls for the four, which go on or leave together
+            if (!vote_all(warp != 0 || warp_wait(acc_full + 8u * buf, (n / 2u) & 1u))) break;
             tc_fence_after();
             if (shared > 0) {
                 uint32_t held[C::kMaxShared][32];
@@ -674,7 +715,7 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
     using C = PairCfg<kF>;
     static int configured[kMaxDevices] = {0};
     const void* fn = (const void*)pair_kernel<kF>;
-    cudaError_t e = set_smem_limit_once(configured, &fn, 1, (int)C::kSmem);
+    cudaError_t e = set_smem_limit_once(configured, &fn, 1, (int)kPairSmem);
     if (e != cudaSuccess) return e;
     const int64_t row_bytes = T::kFp4 ? p.k / 2 : p.k;
     const int64_t col_tiles = mma_scale_col_tiles(p.k / (T::kFp4 ? 16 : 32));
@@ -718,8 +759,16 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
     a.tiles = (uint32_t)(p.a.batch * w_tiles * t_tiles);
     a.per_batch = make_fastdiv((uint32_t)(w_tiles * t_tiles));
     a.per_group = make_fastdiv((uint32_t)w_tiles * kGroup);
+    // as many stages as fit: few tokens leave room for more weight rows in flight
+    a.stage = (C::kW + (uint32_t)a.tile_t / 2u * kStepBytes + 1023u) / 1024u * 1024u;
+    a.scale_stage = (1u + (uint32_t)a.t_band_box) * T::kScaleBytes;
+    const uint32_t out = 2u * C::kOutBufs * kOutBytes;
+    a.stages = std::min<uint32_t>(kMaxStages, (kPairSmem - 1024u - out) / (a.stage + a.scale_stage));
+    a.scale_bufs = T::kFp4 ? 3u : a.stages;
+    a.out_at = a.stages * a.stage;
+    a.scales_at = a.out_at + out;
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(a.tiles, pairs);
-    pair_kernel<kF><<<grid, kPairThreads, C::kSmem, s>>>(a);
+    pair_kernel<kF><<<grid, kPairThreads, 1024u + a.scales_at + a.stages * a.scale_stage, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -91,6 +91,21 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0u;
 }
 
+// Position in a ring of barriers: stage and the parity of its current use.
+struct RingPos {
+    uint32_t at = 0u, phase = 0u;
+    __device__ __forceinline__ void next(uint32_t stages) {
+        if (++at == stages) {
+            at = 0u;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ void prefetch_tensor_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
+}
+
 // ---------------------------------------------------------------- descriptors
 
 // K-major operand tile in shared memory, rows of 128 bytes in the 128-byte
