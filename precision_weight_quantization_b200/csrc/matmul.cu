@@ -669,10 +669,12 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
     a.last_mmas = (int)((row_bytes - (int64_t)(a.steps - 1) * kStepBytes + 31) / 32);
     a.w_tiles = make_fastdiv((uint32_t)w_tiles);
     a.t_tiles = make_fastdiv((uint32_t)t_tiles);
-    // split K while the tiles leave half of the resident CTA slots (two per SM) empty
-    const int64_t slots = 2 * (int64_t)sm_count(current_device());
+    // Split K while the CTAs stay within 4/3 of the SMs and keep 2.5 steps each: at 4096 x 2560 and one token,
+    // 32 tiles in 128 CTAs take 4.9 us (MXFP8), in 256 CTAs 6.2 us; NVFP4 2560 x 4096 in 4 parts of 4 steps
+    // 5.1 us, in 8 of 2 steps 5.9 us.
+    const int64_t sms = sm_count(current_device()), limit = sms + sms / 3;
     a.split = 1;
-    while (a.split < kMaxSplit && tiles * a.split * 2 <= slots && a.split * 2 <= a.steps) a.split *= 2;
+    while (a.split < kMaxSplit && tiles * a.split * 2 <= limit && a.split * 2 * 5 <= a.steps * 2) a.split *= 2;
     if (tiles * a.split > (int64_t)0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * a.split));
@@ -776,12 +778,27 @@ template <ProductFormat kF>
 cudaError_t launch_product(const Product& p, cudaStream_t s) {
     EncodeTiledFn encode = encode_tiled_fn();
     if (!encode) return cudaErrorNotSupported;
-    if (p.a.rows > 64) return launch_pairs<kF>(p, encode, s);
-    // tokens per tile: the smallest MMA width that holds them all, at most 128
-    if (p.a.rows <= 16) return launch_tokens<kF, 16>(p, encode, s);
-    if (p.a.rows <= 32) return launch_tokens<kF, 32>(p, encode, s);
-    if (p.a.rows <= 64) return launch_tokens<kF, 64>(p, encode, s);
-    return launch_tokens<kF, 128>(p, encode, s);
+    const int64_t m = p.a.rows, w_tiles = (p.w.rows + 255) / 256, pairs = sm_count(current_device()) / 2;
+    const int64_t steps = ((kF == ProductFormat::kNvfp4 ? p.k / 2 : p.k) + kStepBytes - 1) / kStepBytes;
+    if (m <= 64) {
+        // One token tile.  The pairs win where they are at least 60 % busy (128 x 1536 x 2048 at 64 tokens:
+        // NVFP4 47 against 62 us, MXFP8 78 against 81), else the finer tiles and the split K of the token
+        // kernel do (19456 x 2560, 76 tiles on 74 pairs: NVFP4 8.5 against 11.2 us at one token).
+        const int64_t tiles = p.a.batch * w_tiles, waves = (tiles + pairs - 1) / pairs;
+        if (5 * tiles >= 3 * waves * pairs) return launch_pairs<kF>(p, encode, s);
+        // tokens per tile: the smallest MMA width that holds them all
+        if (m <= 16) return launch_tokens<kF, 16>(p, encode, s);
+        if (m <= 32) return launch_tokens<kF, 32>(p, encode, s);
+        return launch_tokens<kF, 64>(p, encode, s);
+    }
+    // A few more tokens against few weight rows and a long K: at most 20 pairs would work (2560 x 9728,
+    // MXFP8: 128 tokens 12.7 against 22.6 us, 256 tokens 16.3 against 22.8; 2560 x 4096, NVFP4, 256 tokens the
+    // pairs win, 8.8 against 10.4).
+    if (p.a.batch * w_tiles <= 20) {
+        if (m <= 128 && steps >= 16) return launch_tokens<kF, 64>(p, encode, s);
+        if (m <= 256 && steps >= 32) return launch_tokens<kF, 128>(p, encode, s);
+    }
+    return launch_pairs<kF>(p, encode, s);
 }
 
 }  // namespace
