@@ -65,6 +65,13 @@ def _desc(t: torch.Tensor, name: str, packed: bool = False) -> PwqTensor:
         return PwqTensor(t.data_ptr(), B, M, cols, M * N, N)
     if N > 1 and last != 1:
         raise ValueError("%s: last dimension must be contiguous" % name)
+    if M == 1 or B == 1:      # torch leaves the stride of a dimension of size 1 arbitrary
+        if M == 1:
+            rs = -(-N // 16) * 16
+            if B > 1 and bs < rs:
+                rs = N
+        if B == 1:
+            bs = M * rs
     return PwqTensor(t.data_ptr(), B, M, cols, bs, rs)
 
 
@@ -627,7 +634,8 @@ def _product_out(a, w, out):
     if a.dim() != w.dim():
         raise ValueError("a and w must both be 2-D or both 3-D, got %s and %s" % (tuple(a.shape), tuple(w.shape)))
     if out is None:
-        return torch.empty(a.shape[:-1] + (w.shape[-2],), dtype=torch.bfloat16, device=a.device)
+        # separate sizes: torch parses them 2 us faster than a shape
+        return torch.empty(*a.shape[:-1], w.shape[-2], dtype=torch.bfloat16, device=a.device)
     _check_dtype(out, (torch.bfloat16,), "out")
     return out
 
@@ -687,7 +695,7 @@ def _norm_inputs(x, weight, residual, h):
         return ctypes.byref(dx), None, None, dx, x
     _check_dtype(residual, (torch.bfloat16,), "residual")
     if h is None:
-        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        h = torch.empty(*x.shape, dtype=torch.bfloat16, device=x.device)
     _check_dtype(h, (torch.bfloat16,), "h")
     return ctypes.byref(dx), ctypes.byref(_desc(residual, "residual")), ctypes.byref(_desc(h, "h")), dx, h
 
@@ -705,9 +713,10 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     B, M, S = dx.batch, dx.rows, dx.cols // 32
     n = _tile_bytes(B, M, S) if mma else B * M * S
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = torch.empty(*x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     if scale is None:
-        scale = torch.empty((n,) if mma else x.shape[:-1] + (S,), dtype=torch.uint8, device=x.device)
+        scale = (torch.empty(n, dtype=torch.uint8, device=x.device) if mma else
+                 torch.empty(*x.shape[:-1], S, dtype=torch.uint8, device=x.device))
     _check_dtype(out, _CODE_DTYPES, "out")
     _same_device(x, weight, residual, out, scale, h)
     _launch(x, "rms_norm_mxfp8", px, pr, weight.data_ptr(), eps, ph, ctypes.byref(_desc(out, "out")),
@@ -727,10 +736,10 @@ def rms_norm_nvfp4(x: torch.Tensor, weight: torch.Tensor, amax: torch.Tensor,
     n = _tile_bytes(B, M, S) if mma else B * M * S
     dev = x.device
     if out is None:
-        out = torch.empty(x.shape[:-1] + (dx.cols // 2,), dtype=torch.uint8, device=dev)
+        out = torch.empty(*x.shape[:-1], dx.cols // 2, dtype=torch.uint8, device=dev)
     if sb is None:
-        sb = (torch.empty((n,), dtype=torch.uint8, device=dev) if mma else
-              torch.empty(x.shape[:-1] + (S,), dtype=torch.float8_e4m3fn, device=dev))
+        sb = (torch.empty(n, dtype=torch.uint8, device=dev) if mma else
+              torch.empty(*x.shape[:-1], S, dtype=torch.float8_e4m3fn, device=dev))
     if global_scale is None:
         global_scale = torch.empty(B, dtype=torch.float32, device=dev)
     _check_dtype(out, (torch.uint8,), "out")
@@ -753,9 +762,9 @@ def rms_norm_fake_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optiona
         raise ValueError("amax is given exactly with format='nvfp4'")
     px, pr, ph, dx, h = _norm_inputs(x, weight, residual, h)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(*x.shape, dtype=torch.bfloat16, device=x.device)
     _check_dtype(out, (torch.bfloat16,), "out")
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(*x.shape[:-1], dtype=torch.float32, device=x.device)
     _same_device(x, weight, residual, amax, out, h)
     head = (px, pr, weight.data_ptr(), eps)
     tail = (ph, ctypes.byref(_desc(out, "out")), rstd.data_ptr())
@@ -792,7 +801,7 @@ def _norm_backward(dy, h, weight, rstd, dh, dweight_dtype, out=None):
     """rms_norm_backward of checked arguments (dweight_dtype None: no dweight)."""
     dev = h.device
     if out is None:
-        out = torch.empty(h.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(*h.shape, dtype=torch.bfloat16, device=dev)
     ph = ctypes.byref(_desc(h, "h"))
     dw = None
     pw = pws = None

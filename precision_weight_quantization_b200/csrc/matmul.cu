@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
                 if (!warp_wait(full + 8u * (j % kS), (j / kS) & 1)) break;
     } else if (warp == 5) {
         constexpr uint32_t idesc = mma_idesc<kF>(128, kTok);
+        const uint32_t tok_col = (uint32_t)(t0 % 128) / 32u;   // 64-token tiles: the band's upper half
         const bool leader = elect_one();
         bool ready = false;   // the next operands' barrier, tested while a step is issued
         for (int i = 0; i < steps; ++i) {
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
                     if (j >= mmas) break;
                     const uint32_t id = T::kFp4 ? idesc : idesc | (uint32_t)j << 4 | (uint32_t)j << 29;
                     const uint32_t so = T::kFp4 ? 4u * j : 0u;
-                    mma_block_scaled<kF, 1>(tmem, dw + 2u * j, dx + 2u * j, id, sw + so, sx + so, (i | j) != 0);
+                    mma_block_scaled<kF, 1>(tmem, dw + 2u * j, dx + 2u * j, id, sw + so, sx + so + tok_col,
+                                            (i | j) != 0);
                 }
             }
             ready = mbar_test(full + 8u * nx, ((i + 1) / kS) & 1);

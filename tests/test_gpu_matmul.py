@@ -173,6 +173,31 @@ def test_values_of_wide_products(P, fmt, shape):
     check(P, random_operand(fmt, B, M, K, 3), random_operand(fmt, B, N, K, 4))
 
 
+# one token tile of every width on many weight rows; a few more tokens against few weight rows and a long K
+# (K split over a cluster at 64 and 128 tokens a tile); many tiles of few tokens
+MIDDLE = [(1, 65, 5400, 320), (1, 96, 5400, 288), (1, 130, 5640, 160), (1, 160, 5400, 320), (1, 200, 5400, 352),
+          (1, 224, 5400, 96), (1, 225, 5400, 320), (1, 100, 700, 4160), (1, 200, 300, 8256), (1, 64, 640, 8256),
+          (90, 7, 300, 160), (90, 50, 280, 544), (80, 33, 512, 1312)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("shape", MIDDLE, ids=lambda s: "x".join(map(str, s)))
+def test_values_between_tokens_and_prompts(P, fmt, shape):
+    B, M, N, K = shape
+    check(P, random_operand(fmt, B, M, K, 26), random_operand(fmt, B, N, K, 27))
+
+
+def test_single_rows_with_arbitrary_strides(P):
+    """A dimension of size 1 may carry any stride."""
+    a, w = random_operand("mxfp8", 1, 1, 96, 28), random_operand("mxfp8", 1, 40, 96, 29)
+    ref = check(P, a, w, two_d=True)
+    q, s = a.args(True)
+    odd = torch.as_strided(q.view(torch.uint8), (1, 96), (7, 1))
+    assert torch.equal(P.mxfp8_matmul(odd, s, *w.args(True)), ref)
+    three = torch.as_strided(q.view(torch.uint8), (1, 1, 96), (5, 3, 1))
+    assert torch.equal(P.mxfp8_matmul(three, s, *w.args())[0], ref)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("shape", [(1, 1, 300, 4096), (1, 40, 129, 2080), (2, 130, 257, 1056), (1, 700, 1030, 4096),
                                    (1, 2100, 4100, 800)], ids=lambda s: "x".join(map(str, s)))
