@@ -82,6 +82,11 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 // FP32 partials meet in distributed shared memory and are added in rank
 // order (the result does not depend on timing).
 //
+// Bound by the weight's bytes and, for small weights, by the launch: 19456 x
+// 2560 at one token takes 8.4 us in NVFP4 (28 MB, 3.3 TB/s) and 12.3 us in
+// MXFP8 (51 MB, 4.2 TB/s); 4096 x 2560 takes 4.8 us, where an empty launch of
+// the norm kernel's size takes 2.7.
+//
 // Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales), 5 MMA issuer and TMEM owner.
 
 constexpr int kTokThreads = 224, kMaxSplit = 8;
@@ -106,7 +111,10 @@ struct TokCfg {
     static constexpr uint32_t kW = 128u * kStepBytes, kT = (uint32_t)kTok * kStepBytes;
     static constexpr uint32_t kStage = kW + kT + 2u * T::kScaleBytes;
     // two CTAs per SM: a tile more than there are SMs must not cost a second wave
-    static constexpr int kStages = kTok <= 16 || (kTok == 32 && !T::kFp4) ? 5 : kTok == 32 || (kTok == 64 && !T::kFp4) ? 4 : 3;
+    // (NVFP4, 64 tokens, 152 tiles: 16.7 us with four stages and one CTA per SM, 11.4 us with three and two)
+    static constexpr int kStages = kTok <= 16 || (kTok == 32 && !T::kFp4)  ? 5
+                                   : kTok == 32 || (kTok == 64 && !T::kFp4) ? 4
+                                                                           : 3;
     static constexpr uint32_t kSmem = kStages * kStage + 1024u;   // + alignment of the ring to 1024 bytes
     // TMEM: kTok accumulator columns, then a buffer of weight and token scale columns for each stage
     static constexpr uint32_t kScaleCols = 4u * T::kScaleTiles;
@@ -304,12 +312,24 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
 // that the pairs at work share operands in L2.
 //
-// Tensor memory: 512 columns hold scale buffers of a step each (three for
-// NVFP4, five for MXFP8; a buffer is filled again once the step that read it
-// has been seen to end: with two buffers that wait cost 10 to 13 % of the
-// step) and two accumulators, which overlap where two of 256 columns do not
-// fit: the epilogue takes the shared columns into registers first and then
-// lets the next tile begin.
+// What bounds it: long products, the bytes from L2 to the SMs.  A step takes
+// 0.39 to 0.41 us (MXFP8, 33.5 KB per SM) or 0.47 us (NVFP4, 38 KB, of which 6
+// are scales), 12.1 to 12.6 TB/s over 148 SMs whatever the tile, where its
+// four MMAs take 0.27 us; 8192^3 runs at 2.99 PFLOP/s (MXFP8) and 5.3 (NVFP4).
+// Short K and few tiles: the start of a tile (about 1000 clocks between one
+// tile's last MMA and the next one's first) and whole waves of 74 pairs.
+//
+// Issue: four MMAs of 128 clocks leave 512 clocks for a step's bookkeeping.
+// The issuer tests the next step's barriers while it issues a step and waits
+// only when the test failed (two waits at the start of each step made every
+// step take 0.31 us even at 32 tokens, where it takes 0.07 us now).
+//
+// Tensor memory: 512 columns hold scale buffers of a step each (MXFP8 one per
+// stage of the ring; NVFP4, 48 columns each, three, filled again once the
+// step that read them has been seen to end: with two that wait cost 10 to 13 %
+// of the step) and two accumulators, which overlap where two of 256 columns
+// do not fit: the epilogue takes the shared columns into registers first and
+// then lets the next tile begin.
 //
 // Output: 32 tokens at a time, TMEM fragments are transposed by stmatrix into
 // [token][64 weight rows] boxes (128-byte swizzle, no bank conflicts) and
@@ -320,8 +340,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // starts at a multiple of 64 rows of a 128-row band (and its scales span at
 // most two bands).  The host picks the one with the least work in the last wave.
 //
-// Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales: one warp issuing
-// all four loads took 0.31 us per step), 5 MMA issuer (first CTA) and TMEM owner.
+// Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales), 5 MMA issuer
+// (first CTA) and TMEM owner.
 
 constexpr int kPairThreads = 224;
 constexpr uint32_t kGroup = 8;

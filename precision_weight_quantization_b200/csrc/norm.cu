@@ -32,7 +32,7 @@ enum class NormOut { kMxfp8, kNvfp4, kMxfp8Fake, kNvfp4Fake };
 struct NormArgs {
     View x, res, h, out;         // res.ptr / h.ptr null without a residual
     const uint4* weight;
-    double eps;
+    double eps, d, inv_d;        // D and its reciprocal
     const float* amax;           // NVFP4: [batch]
     float* gs;                   // NVFP4 codes: [batch]
     uint8_t* scale;              // codes: block scales
@@ -60,15 +60,18 @@ __device__ __forceinline__ uint4 add_bf16(uint4 a, uint4 b) {
     return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
 
-__device__ __forceinline__ double add_squares(double s, uint4 v) {
+// The sum of the squares of 8 elements, as two chains (a chain of 64-bit
+// additions over a thread's 32 elements would take longer than its loads).
+__device__ __forceinline__ double squares(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    double lo = 0.0, hi = 0.0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const double lo = (double)bf16_lo(w[i]), hi = (double)bf16_hi(w[i]);
-        s = __fma_rn(lo, lo, s);
-        s = __fma_rn(hi, hi, s);
+        const double a = (double)bf16_lo(w[i]), b = (double)bf16_hi(w[i]);
+        lo = __fma_rn(a, a, lo);
+        hi = __fma_rn(b, b, hi);
     }
-    return s;
+    return lo + hi;
 }
 
 // A 64-bit value as FP32 that rounds to the same BF16: the nearest FP32,
@@ -79,6 +82,28 @@ __device__ __forceinline__ float narrow_for_bf16(float h, float w, double rstd) 
     const double back = (double)f;
     if ((__float_as_uint(f) & 0xffffu) != 0x8000u || back == t) return f;
     return __uint_as_float(__float_as_uint(f) + (fabs(t) > fabs(back) ? 1u : 0xffffffffu));
+}
+
+// s / D from the correctly rounded reciprocal rd of D: a product and one
+// residual correction (Markstein, as div_fast), exact when the quotient is.
+__device__ __forceinline__ double mean_of(double s, double d, double rd) {
+    const double q = __dmul_rn(s, rd);
+    return __fma_rn(__fma_rn(-q, d, s), rd, q);
+}
+
+// v^(-1/2) to 64-bit accuracy for v in [1e-16, 1e80]: v = m 4^k with m in
+// [1, 4), the FP32 rsqrtf of m (error e0 below 2^-20), and one step of
+// Householder's third-order iteration for x^(-1/2), y (1 + e / 2 + 3 e^2 / 8)
+// with e = 1 - m y^2, whose error is of the order e0^3.  A power of four
+// gives its root exactly.  (IEEE square root and division take about 200
+// instructions in every thread, a third of the kernel's.)
+__device__ __forceinline__ double inverse_sqrt(double v) {
+    const int hi = __double2hiint(v), k2 = ((hi >> 20) - 1023) & ~1;
+    const double m = __hiloint2double(hi - (k2 << 20), __double2loint(v));
+    const double y = (double)rsqrtf((float)m);
+    const double e = __fma_rn(-__dmul_rn(m, y), y, 1.0);
+    const double r = __fma_rn(__dmul_rn(y, e), __fma_rn(e, 0.375, 0.5), y);
+    return __hiloint2double(__double2hiint(r) - ((k2 / 2) << 20), __double2loint(r));
 }
 
 // The row's rstd for normalise(): hs = 2^E with E = max(exponent of rstd,
@@ -111,8 +136,8 @@ __device__ __noinline__ uint4 normalise_wide(uint4 hv, uint4 wv, double rstd) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// y = bf16(h rstd weight) of 8 elements.
-__device__ __forceinline__ uint4 normalise(uint4 hv, uint4 wv, const RowScale& rs) {
+// y = bf16(h rstd weight) of 8 elements, and in `mag` per half the largest magnitude of y (amax_word8).
+__device__ __forceinline__ uint4 normalise(uint4 hv, uint4 wv, const RowScale& rs, uint32_t& mag) {
     const uint32_t h[4] = {hv.x, hv.y, hv.z, hv.w}, w[4] = {wv.x, wv.y, wv.z, wv.w};
     uint32_t o[4], low[4];
 #pragma unroll
@@ -127,9 +152,14 @@ __device__ __forceinline__ uint4 normalise(uint4 hv, uint4 wv, const RowScale& r
     uint32_t lo = __vminu2(__vminu2(low[0], low[1]), __vminu2(low[2], low[3]));
     lo = min(lo & 0xffffu, lo >> 16);
     // an infinite y: the product may have left FP32 although the value did not
-    const uint32_t hi = hmax_abs(hmax_abs(o[0], o[1]), hmax_abs(o[2], o[3])) & 0x7fff7fffu;
+    mag = hmax_abs(hmax_abs(o[0], o[1]), hmax_abs(o[2], o[3]));
+    const uint32_t hi = mag & 0x7fff7fffu;
     const bool inf = (hi & 0xffffu) >= 0x7f80u || hi >= 0x7f800000u;
-    if (lo <= 5u || inf || rs.wide) return normalise_wide(hv, wv, rs.rstd);
+    if (lo <= 5u || inf || rs.wide) {
+        const uint4 y = normalise_wide(hv, wv, rs.rstd);
+        mag = amax_word8(y);
+        return y;
+    }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -139,17 +169,18 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// Block scales of one row: `word` (valid in the first lane of every four
-// blocks) holds four consecutive scale bytes, zero past the last column;
-// `byte` this block's own, written by the block's first lane in the dense layout.
-__device__ __forceinline__ void store_scale(const NormArgs& a, uint32_t r, uint32_t b, uint32_t m, int col,
-                                            bool block_lane, bool word_lane, uint32_t byte, uint32_t word) {
-    if (a.sf_mma) {
-        if (word_lane)
-            st_u32(a.scale + (int64_t)b * a.sf_slab + mma_scale_offset(m, (uint32_t)col, a.sf_ct), word);
-    } else if (block_lane) {
-        a.scale[(int64_t)r * a.s_cols + col] = (uint8_t)byte;
+// A block's scale byte, written by one of its lanes: `at` is the row's first
+// byte in the tile layout or the dense one.  The row's last block also writes
+// the zeros that pad its columns to a multiple of four in the tile layout.
+__device__ __forceinline__ void store_scale(const NormArgs& a, uint8_t* at, int col, uint32_t byte) {
+    if (!a.sf_mma) {
+        at[col] = (uint8_t)byte;
+        return;
     }
+    uint8_t* p = at + (uint32_t)(col >> 2) * 512u;
+    p[col & 3] = (uint8_t)byte;
+    if (col == a.s_cols - 1)
+        for (int c = (col & 3) + 1; c < 4; ++c) p[c] = 0u;
 }
 
 // One row per CTA, kVec 8-element vectors per thread, all loaded before any
@@ -158,7 +189,7 @@ __device__ __forceinline__ void store_scale(const NormArgs& a, uint32_t r, uint3
 // neighbouring lanes hold a block: 16-byte loads stay coalesced and the block
 // maximum takes one or two shuffles.
 template <NormOut kOut, int kVec, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxThreads) norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kMx = kOut == NormOut::kMxfp8 || kOut == NormOut::kMxfp8Fake;
     constexpr bool kFake = kOut == NormOut::kMxfp8Fake || kOut == NormOut::kNvfp4Fake;
     const int threads = (int)blockDim.x;
@@ -200,7 +231,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(c
     for (int i = 0; i < kVec; ++i) {
         const int k = i * threads + (int)threadIdx.x;
         wv[i] = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
-        s = add_squares(s, v[i]);
+        s += squares(v[i]);
     }
     s = warp_sum(s);
     if (threads > 32) {
@@ -209,7 +240,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(c
         s = 0.0;
         for (int i = 0; i < threads / 32; ++i) s += part[i];   // the same order in every thread
     }
-    const RowScale rs = row_scale(1.0 / sqrt(s / (double)(8 * a.vecs) + a.eps));
+    const RowScale rs = row_scale(inverse_sqrt(mean_of(s, a.d, a.inv_d) + a.eps));
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = (float)rs.rstd;
 
     float gs = 0.0f, g6 = 0.0f, r6 = 0.0f;
@@ -222,13 +253,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(c
         if (!kFake && m == 0 && threadIdx.x == 0) a.gs[b] = gs;
     }
     char* out = a.out.ptr + (int64_t)b * a.out.bstride + (int64_t)m * a.out.rstride;
+    uint8_t* scales = kFake ? nullptr
+                            : a.scale + (a.sf_mma ? (int64_t)b * a.sf_slab + mma_scale_offset(m, 0u, a.sf_ct)
+                                                  : (int64_t)r * a.s_cols);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         if (i * threads >= a.vecs) break;   // uniform: shuffles below take whole warps
         const int k = i * threads + (int)threadIdx.x;
         const bool on = k < a.vecs;
-        const uint4 y = normalise(v[i], wv[i], rs);   // zeros past the row
-        uint32_t mw = amax_word8(y);
+        uint32_t mw;
+        const uint4 y = normalise(v[i], wv[i], rs, mw);   // zeros past the row
         mw = hmax_abs(mw, __shfl_xor_sync(0xffffffffu, mw, 1));
         if (kMx) mw = hmax_abs(mw, __shfl_xor_sync(0xffffffffu, mw, 2));
         mw &= 0x7fff7fffu;
@@ -249,11 +283,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(c
                 if (on) st_v4(out + 16 * (int64_t)k, fp8_dequant8(c, exp2i(byte8 - 127)));
             } else {
                 if (on) st_v2(out + 8 * (int64_t)k, c);
-                const uint32_t byte = on ? (uint32_t)byte8 : 0u;
-                uint32_t word = byte;
-#pragma unroll
-                for (int j = 1; j < 4; ++j) word |= __shfl_down_sync(0xffffffffu, byte, 4 * j) << (8 * j);
-                store_scale(a, r, b, m, k >> 2, on && (k & 3) == 0, on && (k & 15) == 0, byte, word);
+                if (on && (k & 3) == 0) store_scale(a, scales, k >> 2, (uint32_t)byte8);
             }
         } else {
             const float am = __uint_as_float(amax << 16);
@@ -268,11 +298,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) norm_kernel(c
                 if (on) st_v4(out + 16 * (int64_t)k, dequant_half(c, e4m3_decode(sb), gs));
             } else {
                 if (on) st_u32(out + 4 * (int64_t)k, c);
-                const uint32_t byte = on ? sb : 0u;
-                uint32_t word = byte;
-#pragma unroll
-                for (int j = 1; j < 4; ++j) word |= __shfl_down_sync(0xffffffffu, byte, 2 * j) << (8 * j);
-                store_scale(a, r, b, m, k >> 1, on && (k & 1) == 0, on && (k & 7) == 0, byte, word);
+                if (on && (k & 1) == 0) store_scale(a, scales, k >> 1, sb);
             }
         }
     }
@@ -509,6 +535,10 @@ cudaError_t launch_norm_kind(const NormArgs& a, cudaStream_t s) {
     // few rows leave SMs idle either way: spread each over four times the threads
     if (D <= 8192 && a.total_rows <= (uint32_t)sm_count(current_device()))
         return launch_norm_out<kOut, 1, 1024>(a, norm_threads(D, 1), s);
+    // five vectors per thread where they fill every lane and four do not (2560 columns, 8192 rows to MXFP8: 29.9
+    // against 31.2 us; where both leave lanes over, four are faster: 3584 columns, 16384 rows 70.1 against 72.7)
+    if (D <= 8192 && norm_threads(D, 5) * 5 == a.vecs && norm_threads(D, 4) * 4 > a.vecs)
+        return launch_norm_out<kOut, 5, 256>(a, norm_threads(D, 5), s);
     if (D <= 8192) return launch_norm_out<kOut, 4, 256>(a, norm_threads(D, 4), s);
     return launch_norm_out<kOut, 4, 1024>(a, norm_threads(D, 4), s);
 }
@@ -545,6 +575,8 @@ cudaError_t launch_norm(const Norm& n, cudaStream_t s) {
     a.out = n.out;
     a.weight = static_cast<const uint4*>(n.weight);
     a.eps = n.eps;
+    a.d = (double)n.x.cols;
+    a.inv_d = 1.0 / a.d;
     a.amax = n.amax;
     a.gs = n.gs;
     a.scale = n.scale;

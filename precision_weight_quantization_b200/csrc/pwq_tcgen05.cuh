@@ -7,6 +7,21 @@
 
 namespace pwq {
 
+// Bit of the device error word: a wait inside a block-scaled product gave up.
+constexpr uint32_t kErrMatmulTimeout = 4u;
+
+// ---------------------------------------------------------------- barriers
+
+// Whether the barrier's phase of that parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
 // ---------------------------------------------------------------- tensor memory
 
 // Whole warp.  Writes the TMEM base address of `cols` columns (a power of
