@@ -312,12 +312,13 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
 // that the pairs at work share operands in L2.
 //
-// What bounds it: long products, the bytes from L2 to the SMs.  A step takes
-// 0.39 to 0.41 us (MXFP8, 33.5 KB per SM) or 0.47 us (NVFP4, 38 KB, of which 6
-// are scales), 12.1 to 12.6 TB/s over 148 SMs whatever the tile, where its
-// four MMAs take 0.27 us; 8192^3 runs at 2.99 PFLOP/s (MXFP8) and 5.3 (NVFP4).
-// Short K and few tiles: the start of a tile (about 1000 clocks between one
-// tile's last MMA and the next one's first) and whole waves of 74 pairs.
+// What bounds it.  Long products: the tensor core at the clock that the power
+// limit leaves.  8192^3 runs at 2.99 PFLOP/s (MXFP8, 1.8 times the measured
+// BF16 rate) and 5.3 (NVFP4, 3.3 times); at 4096 x 9728 x 2560 the tensor
+// pipe is active in 81 % (MXFP8) and 58 % (NVFP4) of the cycles.  Short K and
+// few tiles: the start of a tile (about 1000 clocks between one tile's last
+// MMA and the next one's first, against 5100 of NVFP4 MMAs at K = 2560) and
+// whole waves of 74 pairs.
 //
 // Issue: four MMAs of 128 clocks leave 512 clocks for a step's bookkeeping.
 // The issuer tests the next step's barriers while it issues a step and waits
@@ -714,10 +715,10 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
 }
 
 // Tokens per tile of the pair kernel: the fewest (waves of tiles) x (time of
-// a tile).  A step's time goes with the bytes that it brings from L2 (256
-// weight rows, the tile's tokens, scales worth 24 rows), measured as 0.39 /
-// 0.35 / 0.30 us for 256 / 192 / 128 tokens; a tile's start and the part of
-// its epilogue that nothing hides cost about two steps.
+// a tile).  A step was measured at 0.39 / 0.35 / 0.30 us for 256 / 192 / 128
+// tokens, close to the bytes that it brings in (256 weight rows, the tile's
+// tokens, scales worth 24 rows); a tile's start and the part of its epilogue
+// that nothing hides cost about two steps.
 int pair_tile_tokens(int64_t m, int64_t w_tiles, int64_t batch, int64_t pairs, int64_t steps) {
     int best = 256;
     int64_t best_cost = -1;
