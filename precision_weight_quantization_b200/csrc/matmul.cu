@@ -82,10 +82,9 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 // FP32 partials meet in distributed shared memory and are added in rank
 // order (the result does not depend on timing).
 //
-// Bound by the weight's bytes and, for small weights, by the launch: 19456 x
-// 2560 at one token takes 8.4 us in NVFP4 (28 MB, 3.3 TB/s) and 12.3 us in
-// MXFP8 (51 MB, 4.2 TB/s); 4096 x 2560 takes 4.8 us, where an empty launch of
-// the norm kernel's size takes 2.7.
+// Bound by the weight's bytes and, for small weights, by the launch and the
+// first loads' latency: 19456 x 2560 at one token takes 7.0 us in NVFP4
+// (28 MB, 4.0 TB/s), 2560 x 9728 at eight in MXFP8 7.2 us (26 MB, 3.6 TB/s).
 //
 // Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales), 5 MMA issuer and TMEM owner.
 
@@ -164,6 +163,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    let_later_kernels_start();
+    wait_for_earlier_kernels();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_word, 0);
 
     if (warp == 4 || warp == 6) {
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // most two bands).  The host picks the one with the least work in the last wave.
 //
 // Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales), 5 MMA issuer
-// (first CTA) and TMEM owner.
+// (first CTA) and TMEM owner.  Launched in clusters of two.
 
 constexpr int kPairThreads = 224;
 constexpr uint32_t kGroup = 8;
@@ -396,7 +397,7 @@ __device__ __forceinline__ PairTile pair_tile(const PairArgs& a, uint32_t i) {
 }
 
 template <ProductFormat kF>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ PairArgs a) {
     using T = ProductTraits<kF>;
     using C = PairCfg<kF>;
@@ -436,6 +437,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    let_later_kernels_start();
+    wait_for_earlier_kernels();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_word, 0);
 
     if (warp == 4 || warp == 6) {
@@ -699,19 +702,8 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
     a.split = 1;
     while (a.split < kMaxSplit && tiles * a.split * 2 <= limit && a.split * 2 * 5 <= a.steps * 2) a.split *= 2;
     if (tiles * a.split > (int64_t)0x7fffffff) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * a.split));
-    cfg.blockDim = dim3(kTokThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tokens_kernel<kF, kTok>, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_early(tokens_kernel<kF, kTok>, (unsigned)(tiles * a.split), kTokThreads, C::kSmem, s,
+                        (unsigned)a.split, a);
 }
 
 // Tokens per tile of the pair kernel: the fewest (waves of tiles) x (time of
@@ -793,8 +785,7 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
     a.out_at = a.stages * a.stage;
     a.scales_at = a.out_at + out;
     const unsigned grid = 2u * (unsigned)std::min<int64_t>(a.tiles, pairs);
-    pair_kernel<kF><<<grid, kPairThreads, 1024u + a.scales_at + a.stages * a.scale_stage, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(pair_kernel<kF>, grid, kPairThreads, 1024u + a.scales_at + a.stages * a.scale_stage, s, 2u, a);
 }
 
 template <ProductFormat kF>

@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxTh
     constexpr bool kMx = kOut == NormOut::kMxfp8 || kOut == NormOut::kMxfp8Fake;
     constexpr bool kFake = kOut == NormOut::kMxfp8Fake || kOut == NormOut::kNvfp4Fake;
     const int threads = (int)blockDim.x;
+    let_later_kernels_start();
+    wait_for_earlier_kernels();
     if (!kFake && blockIdx.x >= a.row_ctas) {   // zero scales of the rows that pad the last band
         for (uint64_t i = (uint64_t)(blockIdx.x - a.row_ctas) * threads + threadIdx.x; i < a.pad_words;
              i += (uint64_t)(gridDim.x - a.row_ctas) * threads) {
@@ -370,6 +372,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         fence_mbar_init();
     }
     __syncthreads();
+    let_later_kernels_start();
+    wait_for_earlier_kernels();
     const uint64_t pol = l2_policy_evict_first();
     auto fetch = [&](uint32_t r, uint32_t st) {   // one thread of the group
         const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
@@ -497,6 +501,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
 __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* parts, int n_parts, int D, void* dweight,
                                                             int bf16_out) {
     __shared__ float s[32][33];
+    let_later_kernels_start();
+    wait_for_earlier_kernels();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = (int)blockIdx.x * 32 + lane;
     float v = 0.0f;
@@ -525,8 +531,7 @@ int norm_threads(int64_t D, int vec) { return (int)((D / 8 + 32 * vec - 1) / (32
 template <NormOut kOut, int kVec, int kMaxThreads>
 cudaError_t launch_norm_out(const NormArgs& a, int threads, cudaStream_t s) {
     const unsigned pads = a.pad_words ? (unsigned)std::min<uint64_t>((a.pad_words + threads - 1) / threads, 128) : 0u;
-    norm_kernel<kOut, kVec, kMaxThreads><<<a.row_ctas + pads, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(norm_kernel<kOut, kVec, kMaxThreads>, a.row_ctas + pads, (unsigned)threads, 0, s, 1u, a);
 }
 
 template <NormOut kOut>
@@ -607,8 +612,8 @@ cudaError_t launch_bwd_kernel(const NormBwdArgs& a, const BwdShape& sh, cudaStre
     const void* fn = (const void*)norm_bwd_kernel<kVec, kMaxThreads, kMinCtas, kHoldW>;
     const cudaError_t e = set_smem_limit_once(configured, &fn, 1, (int)kBwdSmem);
     if (e != cudaSuccess) return e;
-    norm_bwd_kernel<kVec, kMaxThreads, kMinCtas, kHoldW><<<sh.grid, sh.tpr * sh.groups, sh.smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(norm_bwd_kernel<kVec, kMaxThreads, kMinCtas, kHoldW>, (unsigned)sh.grid,
+                        (unsigned)(sh.tpr * sh.groups), sh.smem, s, 1u, a);
 }
 
 }  // namespace
@@ -643,8 +648,8 @@ cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
                                            : launch_bwd_kernel<2, 1024, 1, false>(a, sh, s);
     if (e != cudaSuccess || !n.dweight) return e;
     const int D = (int)n.h.cols;
-    norm_dweight_kernel<<<(D + 31) / 32, 1024, 0, s>>>(a.parts, sh.grid, D, n.dweight, n.dweight_bf16);
-    return cudaGetLastError();
+    return launch_early(norm_dweight_kernel, (unsigned)((D + 31) / 32), 1024, 0, s, 1u, (const float*)a.parts, sh.grid, D,
+                        n.dweight, n.dweight_bf16);
 }
 
 }  // namespace pwq

@@ -426,3 +426,50 @@ def test_second_derivative_is_refused(P):
     y, h = P.rms_norm_fake_quant_ste(leaf, w, r)
     with pytest.raises(RuntimeError):
         torch.autograd.grad(y.float().square().sum(), leaf, create_graph=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", (1, 200))
+def test_layers_back_to_back(P, fmt, M):
+    """Twelve layers (norm, product, the residual updated in place, small
+    buffers reused) enqueued without a pause give the bits that they give with
+    a synchronisation after every call: kernels that are set up before the
+    one ahead of them has ended still read what it wrote."""
+    D, N = 1024, 1056
+    g = torch.Generator(device=DEV).manual_seed(98)
+    def w(n, k):
+        return (torch.randn(n, k, generator=g, device=DEV) * 0.05).bfloat16()
+    x0 = torch.randn(M, D, generator=g, device=DEV).bfloat16()
+    norm_w = (1 + 0.1 * torch.randn(D, generator=g, device=DEV)).bfloat16()
+    up, down = w(N, D), w(D, N)
+    amax = torch.full((1,), 5.0, device=DEV)
+    if fmt == "mxfp8":
+        (qu, qd), (su, sd) = P.mxfp8_quant_grouped_mma([up, down])
+    else:
+        q, sb, gs = P.nvfp4_quant_grouped_mma([[up], [down]])
+
+    def run(pause):
+        x, res, outs = x0.clone(), x0.clone(), []
+        def step(t):
+            if pause:
+                torch.cuda.synchronize()
+            return t
+        for _ in range(12):
+            if fmt == "mxfp8":
+                c, s, _h = step(P.rms_norm_mxfp8(x, norm_w, res, h=res))
+                mid = step(P.mxfp8_matmul(c, s, qu, su))
+                (c,), (s,) = step(P.mxfp8_quant_grouped_mma([mid]))
+                x = step(P.mxfp8_matmul(c, s, qd, sd))
+            else:
+                c, s, ga, _h = step(P.rms_norm_nvfp4(x, norm_w, amax, res, h=res))
+                mid = step(P.nvfp4_matmul(c, s, ga, q[0][0], sb[0][0], gs[0]))
+                p, b, ga = step(P.nvfp4_quant_grouped_mma([[mid]]))
+                x = step(P.nvfp4_matmul(p[0][0], b[0][0], ga[0], q[1][0], sb[1][0], gs[1]))
+            outs.append(x.clone())
+        outs.append(res)
+        torch.cuda.synchronize()
+        return outs
+
+    want = run(True)
+    for _ in range(8):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
