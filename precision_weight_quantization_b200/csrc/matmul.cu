@@ -354,7 +354,7 @@ struct PairArgs {
     CUtensorMap w, ws, t, ts, y;
     const float* gt;
     const float* gw;
-    uint16_t* yp;                // y_tma == 0: element stores
+    uint16_t* yp;                // y_tma == 0: rows that TMA does not take
     int64_t y_bs, y_rs;          // elements
     int y_tma;
     int n, m;
@@ -394,6 +394,51 @@ __device__ __forceinline__ PairTile pair_tile(const PairArgs& a, uint32_t i) {
     r.tt = (int)(g * kGroup + i - (uint32_t)r.wt * in_group);
     r.b = (int)b;
     return r;
+}
+
+// Stores `rows` (up to 16) token rows of a box, from token 0 or 16 on, as rows
+// of y that TMA does not take: 64 weight rows, `valid` of which exist.  A row
+// is one 128-byte run: a lane stores the aligned word of two elements, and
+// where the row starts in the middle of a word the first lane stores both ends.
+__device__ __forceinline__ void store_rows(uint32_t box, int c, int rows, uint16_t* y, int64_t y_rs, int valid,
+                                           int lane) {
+    box += (uint32_t)c * 128u;
+    auto word = [&](int r) {   // elements 2 lane and 2 lane + 1 of row r
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];"
+                     : "=r"(v)
+                     : "r"(box + r * 128u + ((((uint32_t)lane >> 2) ^ (r & 7u)) * 16u + ((uint32_t)lane & 3u) * 4u)));
+        return v;
+    };
+    if (valid < 64 || rows < 16) {
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t v = word(r);
+            uint16_t* row = y + r * y_rs + 2 * lane;
+            if (2 * lane < valid) row[0] = (uint16_t)v;
+            if (2 * lane + 1 < valid) row[1] = (uint16_t)(v >> 16);
+        }
+        return;
+    }
+    char* at = reinterpret_cast<char*>(y) + 4 * lane;
+    const int64_t pitch = 2 * y_rs;
+#pragma unroll
+    for (int r0 = 0; r0 < 16; r0 += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = word(r0 + r);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            // a row in the middle of a word: elements 2 lane - 1 and 2 lane; the first lane: 63 and 0
+            char* row = at + (r0 + r) * pitch;
+            const uint32_t odd = (uint32_t)(uintptr_t)row & 2u;
+            const uint32_t w = __byte_perm(__shfl_sync(0xffffffffu, v[r], lane + 31), v[r], odd ? 0x5432 : 0x7654);
+            asm volatile(
+                "{\n\t.reg .pred ends;\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tsetp.ne.u32 ends, %2, 0;\n\t"
+                "@!ends st.global.b32 [%0], %1;\n\t@ends st.global.b16 [%0 + 2], hi;\n\t"
+                "@ends st.global.b16 [%0 + 128], lo;\n\t}"
+                :: "l"(row - odd), "r"(w), "r"(lane == 0 ? odd : 0u) : "memory");
+        }
+    }
 }
 
 template <ProductFormat kF>
@@ -557,17 +602,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t buf = n & 1u, acc = row + buf * acc1, free_bar = cluster_addr(acc_free + 8u * buf, 0);
             const int n0 = (p.wt * 2 + (int)rank) * 128, t0 = p.tt * a.tile_t, chunks = a.tile_t / 32;
             const float2 sc = output_scale(a.gt, a.gw, p.b);
-            const int nn = n0 + warp * 32 + lane;
-            uint16_t* yp = a.yp + (int64_t)p.b * a.y_bs + nn;
+            const int x = n0 + (warp >> 1) * 64;   // the warp pair's 64 weight rows
             // shared columns first: the first buffer's last ones, the second buffer's first ones
             auto column = [&](int k) { return 32 * (buf == 0 ? chunks - 1 - k : k); };
             auto load = [&](int k, uint32_t (&v)[32]) {
-                if (a.y_tma) {
-                    tmem_ld_frag32(acc + column(k), v);
-                    tmem_ld_frag32(acc + (16u << 16) + column(k), v + 16);
-                } else {
-                    tmem_ld32(acc + column(k), v);
-                }
+                tmem_ld_frag32(acc + column(k), v);
+                tmem_ld_frag32(acc + (16u << 16) + column(k), v + 16);
             };
             auto release = [&]() {
                 tc_fence_before();
@@ -577,36 +617,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             auto store = [&](int k, const uint32_t (&v)[32]) {
                 const int t = t0 + column(k);
                 if (t >= a.m || n0 >= a.n) return;   // the same for the CTA
-                if (a.y_tma) {
-                    // the buffer was seen free before the previous store's barrier (or is new)
-                    const uint32_t box = out + stores % C::kOutBufs * kOutBytes, dst = box + frag;
-                    ++stores;
+                // the buffer was seen free before the previous store's barrier (or is new)
+                const uint32_t box = out + stores % C::kOutBufs * kOutBytes, dst = box + frag;
+                ++stores;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {   // eight tokens
-                        uint32_t h[4];
+                for (int r = 0; r < 4; ++r) {   // eight tokens
+                    uint32_t h[4];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int e = 16 * (g >> 1) + 4 * r + 2 * (g & 1);
-                            h[g] = pack_bf16x2(scaled<kF>(v[e], sc), scaled<kF>(v[e + 1], sc));
-                        }
-                        stmatrix_trans(dst + r * 1024u, h[0], h[1], h[2], h[3]);
+                    for (int g = 0; g < 4; ++g) {
+                        const int e = 16 * (g >> 1) + 4 * r + 2 * (g & 1);
+                        h[g] = pack_bf16x2(scaled<kF>(v[e], sc), scaled<kF>(v[e + 1], sc));
                     }
+                    stmatrix_trans(dst + r * 1024u, h[0], h[1], h[2], h[3]);
+                }
+                const bool first_warp = (warp & 1) == 0;   // of the pair: its elected lane issues
+                if (a.y_tma) {
                     fence_async_shared();
-                    const bool first_warp = (warp & 1) == 0;   // of the pair: its elected lane issues
                     if (first_warp && elect_one()) bulk_wait_read<C::kOutBufs - 2>();   // the next buffer has been read
-                    __syncwarp();
-                    asm volatile("bar.sync %0, 64;" :: "r"(2 + (warp >> 1)) : "memory");
-                    const int x = n0 + (warp >> 1) * 64;
+                }
+                __syncwarp();
+                asm volatile("bar.sync %0, 64;" :: "r"(2 + (warp >> 1)) : "memory");
+                if (a.y_tma) {
                     if (first_warp && x < a.n && elect_one()) {
                         tma_store_3d(&a.y, box, x, t, p.b);
                         bulk_commit();
                     }
-                    __syncwarp();
-                } else if (nn < a.n) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (t + c < a.m) yp[(int64_t)(t + c) * a.y_rs] = bf16_bits(scaled<kF>(v[c], sc));
+                } else {
+                    const int c0 = (warp & 1) * 16, valid = min(64, a.n - x), rows = min(16, a.m - t - c0);
+                    uint16_t* yp = a.yp + (int64_t)p.b * a.y_bs + x + (int64_t)(t + c0) * a.y_rs;
+                    store_rows(box, c0, rows, yp, a.y_rs, valid, lane);
                 }
+                __syncwarp();
             };
             // the first warp polls for the four, which go on or leave together
             if (!vote_all(warp != 0 || warp_wait(acc_full + 8u * buf, (n / 2u) & 1u))) break;
