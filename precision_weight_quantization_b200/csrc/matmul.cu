@@ -313,18 +313,20 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
 // that the pairs at work share operands in L2.
 //
-// What bounds it.  Long products: the tensor core at the clock that the power
-// limit leaves.  8192^3 runs at 2.99 PFLOP/s (MXFP8, 1.8 times the measured
-// BF16 rate) and 5.3 (NVFP4, 3.3 times); at 4096 x 9728 x 2560 the tensor
-// pipe is active in 81 % (MXFP8) and 58 % (NVFP4) of the cycles.  Short K and
-// few tiles: the start of a tile (about 1000 clocks between one tile's last
-// MMA and the next one's first, against 5100 of NVFP4 MMAs at K = 2560) and
-// whole waves of 74 pairs.
+// What bounds it.  Power: under these products the SMs run at 1.4 to 1.65 GHz,
+// and what saves clocks without saving energy saves no time.  8192^3 runs at
+// 2.84 PFLOP/s (MXFP8, 1.7 times the measured BF16 rate) and 5.5 (NVFP4, 3.4
+// times).  In clocks: a step of MXFP8 takes 512, its MMAs; one of NVFP4 takes
+// 643, what issuing twelve scale copies beside four MMAs takes, and about 800
+// while the epilogue warp of the same scheduler is at work; a tile's start
+// costs 660 and 1040 (its accumulator shares columns with the one before).
+// Issuing the copies from a warp of their own brought the NVFP4 step to 490 to
+// 610 clocks, and the products 1 to 3 % more time.  The loads bound nothing:
+// without them a step takes the same.
 //
-// Issue: four MMAs of 128 clocks leave 512 clocks for a step's bookkeeping.
-// The issuer tests the next step's barriers while it issues a step and waits
-// only when the test failed (two waits at the start of each step made every
-// step take 0.31 us even at 32 tokens, where it takes 0.07 us now).
+// Issue: the issuer tests the next step's barriers while it issues a step and
+// waits only when the test failed (two waits at the start of each step made
+// every step take 0.31 us even at 32 tokens, where it takes 0.07 us now).
 //
 // Tensor memory: 512 columns hold scale buffers of a step each (MXFP8 one per
 // stage of the ring; NVFP4, 48 columns each, three, filled again once the
@@ -335,7 +337,12 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 //
 // Output: 32 tokens at a time, TMEM fragments are transposed by stmatrix into
 // [token][64 weight rows] boxes (128-byte swizzle, no bank conflicts) and
-// stored by TMA, one warp pair per box.
+// stored by TMA, one warp pair per box.  Rows of y that are not 16-byte
+// aligned, or whose length is no multiple of 8 (TMA would write the whole last
+// 16 bytes), are stored from the boxes by the two warps, a word per lane:
+// NVFP4 4096 x 19455 x 2560 took 144 us with an element per lane straight
+// from TMEM, 126 now, and 81 without the stores (unaligned rows make two
+// requests to L2 of each 128 bytes).
 //
 // The token tile is a multiple of 64 columns up to 256, or of 32 when one
 // tile holds every token: the MMA takes scale columns two by two, so a tile
