@@ -404,13 +404,16 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     uint32_t st = 0u, phase = 0u;
     int flip = 0;
     bool alive = true;
+    int waits = a.ring;
     for (uint64_t r64 = first; r64 < a.total_rows; r64 += stride, flip ^= 1) {
         const uint32_t r = (uint32_t)r64;
         const float rstd = __ldg(a.rstd + r);
-        if (alive && !mbar_wait_bounded(full + 8u * st, phase, kNormWaitNs)) {
+        // once a wait has given up the outputs are unspecified: no further copies, and waits only for those in flight
+        if (waits > 0 && !mbar_wait_bounded(full + 8u * st, phase, kNormWaitNs)) {
             atomicOr(&g_norm_error, kErrTmaTimeout);
-            alive = false;   // the outputs are unspecified from here; no further wait
+            alive = false;
         }
+        if (!alive) --waits;
         uint4 vg[kVec], vh[kVec], vd[kVec];
         const uint32_t at = ring + st * stage + 16u * (uint32_t)t;
 #pragma unroll
