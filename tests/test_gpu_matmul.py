@@ -233,6 +233,28 @@ def test_operand_and_output_strides(P, fmt, M):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N", [(70, 5377), (150, 5504), (333, 1001), (400, 1030), (600, 323), (777, 4160)])
+def test_output_rows_at_every_alignment(P, fmt, M, N):
+    """Rows that begin at every element of a 16-byte unit, even and odd row
+    strides, tiles cut on either side; integers, so the sums are exact."""
+    a, w = integer_operand(fmt, 1, M, 160, 50), integer_operand(fmt, 1, N, 160, 51)
+    ref = bf16_exact(bmm64(a.values(), w.values()))[0].to(DEV)
+    for lead, pad in [(i, 0) for i in range(8)] + [(0, 1), (0, 2), (1, 1), (2, 5), (7, 4)]:
+        out = guard.empty((M, N), torch.bfloat16, lead=lead, pad=pad)
+        assert torch.equal(call(P, a, w, two_d=True, out=out), ref), (lead, pad)
+
+
+@pytest.mark.parametrize("M", (4, 40, 400))
+def test_nan_codes_stay_in_their_row(P, M):
+    """E4M3 has NaN codes; a token that holds one is NaN, the others are as without it."""
+    a, w = random_operand("mxfp8", 1, M, 512, 52), random_operand("mxfp8", 1, 260, 512, 53)
+    ref = call(P, a, w)[0]
+    a.codes[0, 1, 77] = 0x7f
+    y = call(P, Operand("mxfp8", a.codes, a.scales), w)[0]
+    assert bool(y[1].isnan().all()) and torch.equal(y[[0] + list(range(2, M))], ref[[0] + list(range(2, M))])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M", (4, 400))
 def test_nan_scales_stay_in_their_row_and_column(P, fmt, M):
     a, w = random_operand(fmt, 1, M, 512, 13), random_operand(fmt, 1, 260, 512, 14)

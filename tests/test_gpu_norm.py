@@ -195,6 +195,34 @@ def test_strides_and_in_place(P, fmt):
             assert bool((t._base[:, 288:] == 9).all())
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", (5, 400))
+def test_rows_that_are_not_finite_leave_the_others(P, fmt, M):
+    """A padded batch may hold anything: NaN, infinities and sums that
+    overflow in one row change nothing in another, forward and backward."""
+    x, w, r = (t.to(DEV) for t in inputs((M, 320), 90))
+    dy = W.random_bf16((M, 320), seed=91, std=0.5, device=DEV)
+    amax = torch.tensor([3.0], device=DEV)
+    bad, keep = [0, 2, 3], [1] + list(range(4, M))
+    xb, rb = x.clone(), r.clone()
+    xb[0, 5], xb[2], xb[3], rb[3] = float("nan"), float("-inf"), 3e38, 3e38
+
+    def run(x, r):
+        if fmt == "mxfp8":
+            q, s, h = P.rms_norm_mxfp8(x, w, residual=r, mma=False)
+        else:
+            q, s, _, h = P.rms_norm_nvfp4(x, w, amax, residual=r, mma=False)
+        y, _, rstd = P.rms_norm_fake_quant(x, w, r, fmt, None if fmt == "mxfp8" else amax)
+        dx, _ = P.rms_norm_backward(dy, h, w, rstd)
+        return q.view(torch.uint8), s.view(torch.uint8), h, y, dx
+
+    for good, got in zip(run(x, r), run(xb, rb)):
+        assert torch.equal(good[keep], got[keep])
+    h = run(xb, rb)[2]
+    assert bool(h[0].isnan()[5]) and bool(torch.isinf(h[2]).all()) and bool(torch.isinf(h[3]).all())
+    assert len(bad) + len(keep) == M and P.device_error() == 0
+
+
 def test_empty(P):
     w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
