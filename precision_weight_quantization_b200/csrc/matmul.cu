@@ -799,8 +799,9 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
                    (uint32_t)a.t_band_box))
         return cudaErrorInvalidValue;
     // output by TMA where its rows are whole 16-byte units at 16-byte addresses (a store that ends inside a
-    // unit overwrites the rest of it), else element by element
-    a.y_tma = p.y.cols % 8 == 0 && (uintptr_t)p.y.ptr % 16 == 0 && p.y.rstride % 16 == 0 && (p.y.batch == 1 || p.y.bstride % 16 == 0);
+    // unit overwrites the rest of it), else by the epilogue's warps
+    a.y_tma = p.y.cols % 8 == 0 && (uintptr_t)p.y.ptr % 16 == 0 && p.y.rstride % 16 == 0 &&
+              (p.y.batch == 1 || p.y.bstride % 16 == 0);
     if (a.y_tma) {
         const cuuint64_t dims[3] = {(cuuint64_t)p.y.cols, (cuuint64_t)p.y.rows, (cuuint64_t)p.y.batch};
         const cuuint64_t strides[2] = {(cuuint64_t)p.y.rstride,
