@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxTh
             else quotients8<false>(y, d, 0.0f, q);
             const uint32_t c = e2m1x8(q);
             if (kFake) {
-                if (on) st_v4(out + 16 * (int64_t)k, dequant_half(c, e4m3_decode(sb), gs));
+                if (on) st_v4(out + 16 * (int64_t)k, dequant_half_h(c, e4m3x2_f16x2(sb * 0x0101u), f32x2(gs, gs)));
             } else {
                 if (on) st_u32(out + 4 * (int64_t)k, c);
                 if (on && (k & 1) == 0) store_scale(a, scales, k >> 1, sb);
