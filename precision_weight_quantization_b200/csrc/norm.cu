@@ -355,9 +355,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return v;
 }
 
-//
-// kHoldW: the weight stays in registers (128 a thread up to 512 threads);
-// wider rows read it again from L1, so that 1024 threads do not spill.
+// kHoldW: the weight stays in registers where 122 of them fit; else it is read
+// again from L1, so that nothing spills.  A row's chain of waits (its copy, its
+// sums, the barrier) is what keeps the kernel from HBM's rate, hence rstd
+// loaded a row ahead and several CTAs per SM where registers allow: 16384 x
+// 7168 with dh takes 144 us (940 MB, 6.5 TB/s), 16384 x 4096 87 us.
 template <int kVec, int kMaxThreads, int kMinCtas, bool kHoldW>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
     extern __shared__ __align__(128) uint8_t smem_rows[];
@@ -562,23 +564,30 @@ cudaError_t launch_norm_kind(const NormArgs& a, cudaStream_t s) {
     return launch_norm_out<kOut, 4, 1024>(a, norm_threads(D, 4), s);
 }
 
-// Launch shape of the backward pass: two vectors per thread while 1024 threads
-// hold the row, four above; small rows share a CTA of about 256 threads (one
-// dweight part per CTA), and as many rows ahead as shared memory holds.
+// Launch shape of the backward pass: two vectors per thread while 512 threads
+// hold the row, four above (4096 x 12288: 94 us, 123 with two and 1024
+// threads); small rows share a CTA of about 256 threads (one dweight part per
+// CTA), and as many rows ahead as pay.
 struct BwdShape {
     int vec, tpr, groups, ctas, ring, grid;
     size_t smem;
 };
 constexpr size_t kBwdSmem = 200 * 1024;   // per SM
+constexpr int kBwdPairThreads = 320;
 BwdShape norm_bwd_shape(int64_t rows, int64_t D) {
     BwdShape s;
-    s.vec = D <= 16384 ? 2 : 4;
+    s.vec = D <= 8192 ? 2 : 4;
     s.tpr = norm_threads(D, s.vec);
     s.groups = std::max(1, std::min(kMaxGroups, 256 / s.tpr));
     const int threads = s.tpr * s.groups;
-    s.ctas = std::max(1, 512 / threads);   // 128 registers a thread
+    // 512 threads of 128 registers, or two CTAs of up to 320 threads with about 100 (16384 x 4112: 94.8 us, one CTA
+    // per SM 116.7; 16384 x 5120: 115 against 119)
+    s.ctas = s.vec == 2 && threads > 256 && threads <= kBwdPairThreads ? 2 : std::max(1, 512 / threads);
     const size_t stage = 6 * (size_t)D * s.groups;
-    s.ring = (int)std::max<size_t>(1, std::min<size_t>(kMaxRing, kBwdSmem / s.ctas / stage));
+    // several CTAs per SM hide each other's waits: two rows each (16384 x 4096: 86.5 us, 91.6 with four); one alone
+    // needs more (16384 x 7168: 143.7 us with four, 146.9 with two)
+    const size_t most = s.ctas > 1 ? 2 : kMaxRing;
+    s.ring = (int)std::max<size_t>(1, std::min<size_t>(most, kBwdSmem / s.ctas / stage));
     s.smem = s.ring * stage;
     s.grid = persistent_grid((rows + s.groups - 1) / s.groups, s.ctas);
     return s;
@@ -656,10 +665,11 @@ cudaError_t launch_norm_bwd(const NormBwd& n, cudaStream_t s) {
     a.tpr = sh.tpr;
     a.ring = sh.ring;
     const int threads = sh.tpr * sh.groups;
-    const cudaError_t e = sh.vec == 4       ? launch_bwd_kernel<4, 1024, 1, false>(a, sh, s)
-                          : threads <= 256 ? launch_bwd_kernel<2, 256, 2, true>(a, sh, s)
-                          : threads <= 512 ? launch_bwd_kernel<2, 512, 1, true>(a, sh, s)
-                                           : launch_bwd_kernel<2, 1024, 1, false>(a, sh, s);
+    const cudaError_t e = sh.vec == 4  ? threads <= 512 ? launch_bwd_kernel<4, 512, 1, false>(a, sh, s)
+                                                       : launch_bwd_kernel<4, 1024, 1, false>(a, sh, s)
+                          : threads <= 256             ? launch_bwd_kernel<2, 256, 2, true>(a, sh, s)
+                          : threads <= kBwdPairThreads ? launch_bwd_kernel<2, kBwdPairThreads, 2, false>(a, sh, s)
+                                                       : launch_bwd_kernel<2, 512, 1, true>(a, sh, s);
     if (e != cudaSuccess || !n.dweight) return e;
     const int D = (int)n.h.cols;
     return launch_early(norm_dweight_kernel, (unsigned)((D + 31) / 32), 1024, 0, s, 1u, (const float*)a.parts, sh.grid, D,
