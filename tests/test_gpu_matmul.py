@@ -244,6 +244,18 @@ def test_output_rows_at_every_alignment(P, fmt, M, N):
         assert torch.equal(call(P, a, w, two_d=True, out=out), ref), (lead, pad)
 
 
+@pytest.mark.parametrize("N", (33000, 33001))
+def test_outputs_past_32_bits(P, N):
+    """2^31 elements end inside y; both ways to store a row."""
+    M = 66000
+    a, w = integer_operand("mxfp8", 1, M, 64, 54), integer_operand("mxfp8", 1, N, 64, 55)
+    y = call(P, a, w)[0]
+    at = 2 ** 31 // N
+    rows = torch.tensor([0, 1, at - 1, at, at + 1, at + 300, M - 2, M - 1])
+    few = Operand("mxfp8", a.codes[:, rows], a.scales[:, rows])
+    assert torch.equal(y[rows.to(DEV)].cpu(), bf16_exact(bmm64(few.values(), w.values()))[0])
+
+
 @pytest.mark.parametrize("M", (4, 40, 400))
 def test_nan_codes_stay_in_their_row(P, M):
     """E4M3 has NaN codes; a token that holds one is NaN, the others are as without it."""

@@ -223,6 +223,26 @@ def test_rows_that_are_not_finite_leave_the_others(P, fmt, M):
     assert len(bad) + len(keep) == M and P.device_error() == 0
 
 
+def test_rows_past_32_bits(P):
+    """2^31 elements end inside x: the rows around them and the last ones are
+    those of a call on these rows alone."""
+    M, D = 300000, 7200
+    x = torch.empty(M, D, dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(92))
+    w = W.random_bf16((1, D), seed=93, std=1.0, device=DEV)[0]
+    at = 2 ** 31 // D
+    rows = torch.tensor([0, at - 1, at, at + 1, at + 700, M - 1], device=DEV)
+    few = x[rows].contiguous()
+    q, s, _ = P.rms_norm_mxfp8(x, w, mma=False)
+    q1, s1, _ = P.rms_norm_mxfp8(few, w, mma=False)
+    assert torch.equal(q.view(torch.uint8)[rows], q1.view(torch.uint8)) and torch.equal(s[rows], s1)
+    del q
+    y, _, rstd = P.rms_norm_fake_quant(x, w)
+    dx, _ = P.rms_norm_backward(y, x, w, rstd, need_dweight=False)
+    y1, _, rstd1 = P.rms_norm_fake_quant(few, w)
+    dx1, _ = P.rms_norm_backward(y1, few, w, rstd1, need_dweight=False)
+    assert torch.equal(y[rows], y1) and torch.equal(rstd[rows], rstd1) and torch.equal(dx[rows], dx1)
+
+
 def test_empty(P):
     w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
