@@ -75,6 +75,12 @@ def _desc(t: torch.Tensor, name: str, packed: bool = False) -> PwqTensor:
     return PwqTensor(t.data_ptr(), B, M, cols, bs, rs)
 
 
+def _new_desc(t: torch.Tensor, like: PwqTensor, cols: int) -> PwqTensor:
+    """_desc of a tensor just allocated with like's batch and rows (a third of its time)."""
+    n = t.shape[-1]
+    return PwqTensor(t.data_ptr(), like.batch, like.rows, cols, like.rows * n, n)
+
+
 def _lead(x: torch.Tensor):
     return tuple(x.shape[:-2]) if x.dim() == 3 else ()
 
@@ -630,14 +636,16 @@ def _floats(t: torch.Tensor, n: int, name: str) -> int:
     return t.data_ptr()
 
 
-def _product_out(a, w, out):
+def _product_out(a, w, da, dw, out):
+    """The output and its descriptor."""
     if a.dim() != w.dim():
         raise ValueError("a and w must both be 2-D or both 3-D, got %s and %s" % (tuple(a.shape), tuple(w.shape)))
     if out is None:
         # separate sizes: torch parses them 2 us faster than a shape
-        return torch.empty(*a.shape[:-1], w.shape[-2], dtype=torch.bfloat16, device=a.device)
+        out = torch.empty(*a.shape[:-1], w.shape[-2], dtype=torch.bfloat16, device=a.device)
+        return out, _new_desc(out, da, dw.rows)
     _check_dtype(out, (torch.bfloat16,), "out")
-    return out
+    return out, _desc(out, "out")
 
 
 def mxfp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -650,9 +658,9 @@ def mxfp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
     are not differentiable."""
     _check_dtype(a, _CODE_DTYPES, "a")
     _check_dtype(w, _CODE_DTYPES, "w")
-    out = _product_out(a, w, out)
+    da, dw = _desc(a, "a"), _desc(w, "w")
+    out, dy = _product_out(a, w, da, dw, out)
     _same_device(a, a_scale, w, w_scale, out)
-    da, dw, dy = _desc(a, "a"), _desc(w, "w"), _desc(out, "out")
     S = da.cols // 32
     _launch(a, "mxfp8_matmul", ctypes.byref(da), _one_byte(a_scale, _tile_bytes(da.batch, da.rows, S), "a_scale", "tile"),
             ctypes.byref(dw), _one_byte(w_scale, _tile_bytes(da.batch, dw.rows, S), "w_scale", "tile"),
@@ -669,9 +677,9 @@ def nvfp4_matmul(a: torch.Tensor, a_sb: torch.Tensor, a_global_scale: torch.Tens
     scales [B].  As mxfp8_matmul otherwise."""
     _check_dtype(a, (torch.uint8,), "a")
     _check_dtype(w, (torch.uint8,), "w")
-    out = _product_out(a, w, out)
+    da, dw = _desc(a, "a", True), _desc(w, "w", True)
+    out, dy = _product_out(a, w, da, dw, out)
     _same_device(a, a_sb, a_global_scale, w, w_sb, w_global_scale, out)
-    da, dw, dy = _desc(a, "a", True), _desc(w, "w", True), _desc(out, "out")
     B, S = da.batch, da.cols // 16
     _launch(a, "nvfp4_matmul", ctypes.byref(da), _one_byte(a_sb, _tile_bytes(B, da.rows, S), "a_sb", "tile"),
             _floats(a_global_scale, B, "a_global_scale"), ctypes.byref(dw),
@@ -696,8 +704,11 @@ def _norm_inputs(x, weight, residual, h):
     _check_dtype(residual, (torch.bfloat16,), "residual")
     if h is None:
         h = torch.empty(*x.shape, dtype=torch.bfloat16, device=x.device)
-    _check_dtype(h, (torch.bfloat16,), "h")
-    return ctypes.byref(dx), ctypes.byref(_desc(residual, "residual")), ctypes.byref(_desc(h, "h")), dx, h
+        dh = _new_desc(h, dx, dx.cols)
+    else:
+        _check_dtype(h, (torch.bfloat16,), "h")
+        dh = _desc(h, "h")
+    return ctypes.byref(dx), ctypes.byref(_desc(residual, "residual")), ctypes.byref(dh), dx, h
 
 
 def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -714,12 +725,15 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     n = _tile_bytes(B, M, S) if mma else B * M * S
     if out is None:
         out = torch.empty(*x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        do = _new_desc(out, dx, dx.cols)
+    else:
+        _check_dtype(out, _CODE_DTYPES, "out")
+        do = _desc(out, "out")
     if scale is None:
         scale = (torch.empty(n, dtype=torch.uint8, device=x.device) if mma else
                  torch.empty(*x.shape[:-1], S, dtype=torch.uint8, device=x.device))
-    _check_dtype(out, _CODE_DTYPES, "out")
     _same_device(x, weight, residual, out, scale, h)
-    _launch(x, "rms_norm_mxfp8", px, pr, weight.data_ptr(), eps, ph, ctypes.byref(_desc(out, "out")),
+    _launch(x, "rms_norm_mxfp8", px, pr, weight.data_ptr(), eps, ph, ctypes.byref(do),
             _one_byte(scale, n, "scale", "tile" if mma else "dense"), int(mma), None)
     return out, scale, h
 
@@ -737,15 +751,18 @@ def rms_norm_nvfp4(x: torch.Tensor, weight: torch.Tensor, amax: torch.Tensor,
     dev = x.device
     if out is None:
         out = torch.empty(*x.shape[:-1], dx.cols // 2, dtype=torch.uint8, device=dev)
+        do = _new_desc(out, dx, dx.cols)
+    else:
+        _check_dtype(out, (torch.uint8,), "out")
+        do = _desc(out, "out", True)
     if sb is None:
         sb = (torch.empty(n, dtype=torch.uint8, device=dev) if mma else
               torch.empty(*x.shape[:-1], S, dtype=torch.float8_e4m3fn, device=dev))
     if global_scale is None:
         global_scale = torch.empty(B, dtype=torch.float32, device=dev)
-    _check_dtype(out, (torch.uint8,), "out")
     _same_device(x, weight, residual, amax, out, sb, global_scale, h)
     _launch(x, "rms_norm_nvfp4", px, pr, weight.data_ptr(), eps, _floats(amax, B, "amax"), ph,
-            ctypes.byref(_desc(out, "out", True)), _one_byte(sb, n, "sb", "tile" if mma else "dense"), int(mma),
+            ctypes.byref(do), _one_byte(sb, n, "sb", "tile" if mma else "dense"), int(mma),
             _floats(global_scale, B, "global_scale"), None)
     return out, sb, global_scale, h
 
@@ -763,11 +780,14 @@ def rms_norm_fake_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optiona
     px, pr, ph, dx, h = _norm_inputs(x, weight, residual, h)
     if out is None:
         out = torch.empty(*x.shape, dtype=torch.bfloat16, device=x.device)
-    _check_dtype(out, (torch.bfloat16,), "out")
+        do = _new_desc(out, dx, dx.cols)
+    else:
+        _check_dtype(out, (torch.bfloat16,), "out")
+        do = _desc(out, "out")
     rstd = torch.empty(*x.shape[:-1], dtype=torch.float32, device=x.device)
     _same_device(x, weight, residual, amax, out, h)
     head = (px, pr, weight.data_ptr(), eps)
-    tail = (ph, ctypes.byref(_desc(out, "out")), rstd.data_ptr())
+    tail = (ph, ctypes.byref(do), rstd.data_ptr())
     if format == "mxfp8":
         _launch(x, "rms_norm_mxfp8_fake_quant", *head, *tail)
     else:
@@ -800,9 +820,13 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
 def _norm_backward(dy, h, weight, rstd, dh, dweight_dtype, out=None):
     """rms_norm_backward of checked arguments (dweight_dtype None: no dweight)."""
     dev = h.device
+    dhh = _desc(h, "h")
+    ph = ctypes.byref(dhh)
     if out is None:
         out = torch.empty(*h.shape, dtype=torch.bfloat16, device=dev)
-    ph = ctypes.byref(_desc(h, "h"))
+        do = _new_desc(out, dhh, dhh.cols)
+    else:
+        do = _desc(out, "out")
     dw = None
     pw = pws = None
     n = 0
@@ -813,7 +837,7 @@ def _norm_backward(dy, h, weight, rstd, dh, dweight_dtype, out=None):
         pw, pws = dw.data_ptr(), ws.data_ptr()
     _launch(h, "rms_norm_backward", ctypes.byref(_desc(dy, "dy")),
             ctypes.byref(_desc(dh, "dh")) if dh is not None else None, ph, weight.data_ptr(), rstd.data_ptr(),
-            ctypes.byref(_desc(out, "out")), pw, int(dweight_dtype == torch.bfloat16), pws, n)
+            ctypes.byref(do), pw, int(dweight_dtype == torch.bfloat16), pws, n)
     return out, dw
 
 
