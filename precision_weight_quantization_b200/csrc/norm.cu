@@ -362,6 +362,8 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 // 7168 with dh takes 144 us (940 MB, 6.5 TB/s), 16384 x 4096 87 us.
 template <int kVec, int kMaxThreads, int kMinCtas, bool kHoldW>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+    // 1024 threads have 64 registers each: the second pass reads the row from shared memory again
+    constexpr bool kReread = kMaxThreads > 512;
     extern __shared__ __align__(128) uint8_t smem_rows[];
     __shared__ float part[2][kMaxThreads / 32];
     __shared__ __align__(8) uint64_t bars[kMaxGroups * kMaxRing];
@@ -424,27 +426,33 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             alive = false;
         }
         if (!alive) --waits;
-        uint4 vg[kVec], vh[kVec], vd[kVec];
+        constexpr int kKept = kReread ? 1 : kVec;
+        uint4 vg[kKept], vh[kKept], vd[kKept];
         const uint32_t at = ring + st * stage + 16u * (uint32_t)t;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        auto load = [&](int i, int k, bool with_dh) {   // vector i into place k
             const bool on = i * tpr + t < a.vecs;
             const uint32_t o = at + 16u * (uint32_t)(i * tpr);
-            vg[i] = on ? ld_shared_v4(o) : make_uint4(0u, 0u, 0u, 0u);
-            vh[i] = on ? ld_shared_v4(o + row_bytes) : make_uint4(0u, 0u, 0u, 0u);
-            vd[i] = on && has_dh ? ld_shared_v4(o + 2u * row_bytes) : make_uint4(0u, 0u, 0u, 0u);
+            vg[k] = on ? ld_shared_v4(o) : make_uint4(0u, 0u, 0u, 0u);
+            vh[k] = on ? ld_shared_v4(o + row_bytes) : make_uint4(0u, 0u, 0u, 0u);
+            vd[k] = on && with_dh ? ld_shared_v4(o + 2u * row_bytes) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        if constexpr (!kReread) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) load(i, i, has_dh);
         }
         float c = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i0 = 0; i0 < kVec; ++i0) {
+            const int i = kReread ? 0 : i0;
+            if (kReread) load(i0, 0, false);
             const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
-            const uint4 wv = kHoldW ? held[kHoldW ? i : 0] : weight(i);
+            const uint4 wv = kHoldW ? held[kHoldW ? i0 : 0] : weight(i0);
             const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float t0 = bf16_lo(g[j]) * (bf16_lo(hh[j]) * rstd), t1 = bf16_hi(g[j]) * (bf16_hi(hh[j]) * rstd);
-                dw[i][2 * j] += t0;
-                dw[i][2 * j + 1] += t1;
+                dw[i0][2 * j] += t0;
+                dw[i0][2 * j + 1] += t1;
                 c = __fmaf_rn(t0, bf16_lo(w[j]), c);
                 c = __fmaf_rn(t1, bf16_hi(w[j]), c);
             }
@@ -455,7 +463,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         if (warps > 1) asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "r"(tpr) : "memory");
         else __syncwarp();
         const uint64_t next = r64 + (uint64_t)a.ring * stride;
-        if (t == 0 && alive && next < a.total_rows) fetch((uint32_t)next, st);
+        const uint32_t used = st;
+        if (!kReread && t == 0 && alive && next < a.total_rows) fetch((uint32_t)next, used);
         if (++st == (uint32_t)a.ring) {
             st = 0u;
             phase ^= 1u;
@@ -471,10 +480,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         const uint32_t b = fdiv(r, a.rows), m = r - b * a.rows.d;
         char* dx = a.dx.ptr + (int64_t)b * a.dx.bstride + (int64_t)m * a.dx.rstride + 16 * t;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            if (i * tpr + t >= a.vecs) continue;
+        for (int i0 = 0; i0 < kVec; ++i0) {
+            if (i0 * tpr + t >= a.vecs) continue;
+            const int i = kReread ? 0 : i0;
+            if (kReread) load(i0, 0, has_dh);
             const uint32_t g[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w}, hh[4] = {vh[i].x, vh[i].y, vh[i].z, vh[i].w};
-            const uint4 wv = kHoldW ? held[kHoldW ? i : 0] : weight(i);
+            const uint4 wv = kHoldW ? held[kHoldW ? i0 : 0] : weight(i0);
             const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w}, d[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
             uint32_t o[4];
 #pragma unroll
@@ -483,7 +494,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
                 const float e1 = __fmaf_rn(bf16_hi(hh[j]) * rstd, -c, bf16_hi(g[j]) * bf16_hi(w[j]));
                 o[j] = pack_bf16x2(__fmaf_rn(e0, rstd, bf16_lo(d[j])), __fmaf_rn(e1, rstd, bf16_hi(d[j])));
             }
-            st_v4(dx + (int64_t)16 * (i * tpr), make_uint4(o[0], o[1], o[2], o[3]));
+            st_v4(dx + (int64_t)16 * (i0 * tpr), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        if (kReread) {   // the stage has been read by all only now
+            asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "r"(tpr) : "memory");
+            if (t == 0 && alive && next < a.total_rows) fetch((uint32_t)next, used);
         }
     }
     if (!a.parts) return;
