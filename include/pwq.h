@@ -461,6 +461,11 @@ pwq_status nvfp4_matmul(const pwq_tensor* a_packed, const uint8_t* a_sb_mma, con
  * bit for bit (the *_fake_quant forms: their dequantised BF16 values).  y
  * is the BF16 nearest to the product of h, weight and the 64-bit rstd of the
  * exact sum of squares, so the codes do not depend on an order of addition.
+ * Rows that are not finite follow the same formulas and leave the others as
+ * they are: NaN in h makes rstd and the row of y NaN; an infinite h (x +
+ * residual may overflow) makes rstd 0, y 0 where h is finite and NaN where it
+ * is not.  NaN has E4M3 codes; E2M1 has none, so NVFP4 shows it in a block's
+ * scale, and only where the whole block is NaN.
  *
  * x         BF16 [B][M][D], D % 32 == 0 (MXFP8) / % 16 == 0 (NVFP4), D <= 32768.
  * residual  BF16 like x, or NULL.  weight: BF16 [D], 16-byte aligned.

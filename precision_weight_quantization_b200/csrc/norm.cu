@@ -106,9 +106,20 @@ __device__ __forceinline__ double inverse_sqrt(double v) {
     return __hiloint2double(__double2hiint(r) - ((k2 / 2) << 20), __double2loint(r));
 }
 
+// The row's rstd from its sum of squares.  inverse_sqrt works on exponent bits,
+// so a sum that is not finite is answered here: infinite (h holds an infinity,
+// perhaps of a sum x + residual that overflowed) gives 0, NaN gives NaN.  Two
+// selects beside the chain, no branch: one row of 2560 takes 2.0 us, 2.3 with one.
+__device__ __forceinline__ double rstd_of(double sum, double d, double inv_d, double eps) {
+    const double r = inverse_sqrt(mean_of(sum, d, inv_d) + eps);
+    const uint32_t hi = (uint32_t)__double2hiint(sum);
+    const bool finite = hi < 0x7ff00000u, inf = hi == 0x7ff00000u && __double2loint(sum) == 0;
+    return __hiloint2double(finite ? __double2hiint(r) : inf ? 0 : 0x7ff80000, finite ? __double2loint(r) : 0);
+}
+
 // The row's rstd for normalise(): hs = 2^E with E = max(exponent of rstd,
 // -16) (h 2^E is then a multiple of 2^-149, exact), m = fl(rstd 2^-E).
-// Rows whose rstd is below 2^-60 form every product in 64 bits.
+// Rows whose rstd is below 2^-60, zero or NaN form every product in 64 bits.
 struct RowScale {
     double rstd;
     uint64_t hs2, m2;   // {hs, hs}, {m, m}
@@ -122,7 +133,8 @@ __device__ __forceinline__ RowScale row_scale(double rstd) {
     const float m = (float)(rstd * __hiloint2double((1023 - E) << 20, 0));
     r.hs2 = f32x2(hs, hs);
     r.m2 = f32x2(m, m);
-    r.wide = rstd < 0x1p-60;
+    // not in [2^-60, infinity): rstd is zero or positive, so its upper word orders it
+    r.wide = (uint32_t)__double2hiint(rstd) - (963u << 20) >= (2047u - 963u) << 20;
     return r;
 }
 
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxTh
             for (int i = 0; i < threads / 32; ++i) s += part[i];
         }
     }
-    const RowScale rs = row_scale(inverse_sqrt(mean_of(s, a.d, a.inv_d) + a.eps));
+    const RowScale rs = row_scale(rstd_of(s, a.d, a.inv_d, a.eps));
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = (float)rs.rstd;
 
     float gs = 0.0f, g6 = 0.0f, r6 = 0.0f;

@@ -223,6 +223,46 @@ def test_rows_that_are_not_finite_leave_the_others(P, fmt, M):
     assert len(bad) + len(keep) == M and P.device_error() == 0
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,D", [(7, 320), (400, 2560), (7, 8224)])
+def test_rows_that_are_not_finite_follow_the_definition(P, fmt, M, D):
+    """rstd and y of the rows themselves: NaN in h makes the whole row NaN, an
+    infinite h (from an input, or a sum that overflows BF16) makes rstd 0, y 0
+    where h is finite and NaN where it is not.  NaN shows as E4M3 NaN codes, or
+    as an NVFP4 block scale of NaN where the whole block is NaN; E2M1 codes have none."""
+    x, w, r = (t.to(DEV) for t in inputs((M, D), 97))
+    x[0, 5] = float("nan")                      # in the input
+    x[1, 0], r[1, 0] = float("inf"), float("-inf")
+    x[2], r[2] = 3e38, 3e38                     # every sum overflows
+    x[3, 40], r[3, 40] = 3e38, 3e38             # one sum overflows
+    x[4, :] = float("-inf")
+    h = (x.float() + r.float()).bfloat16()
+    rstd = 1 / torch.sqrt(h.double().square().sum(-1, keepdim=True) / D + 1e-6)
+    y = (h.double() * w.double() * rstd)[:5]
+    nan = y.isnan()
+    assert bool(nan[0].all() and nan[1].all() and nan[2].all() and nan[4].all()) and int(nan[3].sum()) == 1
+    amax = torch.tensor([3.0], device=DEV)
+    yq, hq, got = P.rms_norm_fake_quant(x, w, r, fmt, None if fmt == "mxfp8" else amax)
+    assert torch.equal(hq.nan_to_num(7.0), h.nan_to_num(7.0))
+    assert bool(got[:2].isnan().all()) and bool((got[2:5] == 0).all())
+    whole = [0, 1, 2, 4]
+    assert bool(yq[whole].isnan().all()) and bool((yq[3][~nan[3]] == 0).all())
+    if fmt == "mxfp8":
+        assert bool(yq[3][nan[3]].isnan().all())
+        q, s, _ = P.rms_norm_mxfp8(x, w, residual=r, mma=False)
+        assert torch.equal(q.view(torch.uint8)[:5] & 0x7f == 0x7f, nan)
+        assert bool((q.view(torch.uint8)[3][~nan[3]] & 0x7f == 0).all())
+    else:
+        q, s, _, _ = P.rms_norm_nvfp4(x, w, amax, residual=r, mma=False)
+        assert bool((s.view(torch.uint8)[whole] == 0x7f).all()) and bool((s.view(torch.uint8)[3] == 0).all())
+        assert bool((q[3] & 0x77 == 0).all())
+    # the rows after them are finite, and the bad rows' gradients are NaN by the formula
+    assert bool(got[5:].isfinite().all()) and bool(yq[5:].isfinite().all())
+    dy = W.random_bf16((M, D), seed=98, std=0.5, device=DEV)
+    dx, dw = P.rms_norm_backward(dy, hq, w, got)
+    assert bool(dx[:5].isnan().all()) and bool(dx[5:].isfinite().all()) and bool(dw.isnan().all())
+
+
 def test_rows_past_32_bits(P):
     """2^31 elements end inside x: the rows around them and the last ones are
     those of a call on these rows alone."""
