@@ -55,7 +55,7 @@ __device__ __forceinline__ bool vote_all(bool ok) {
 // is 1 unless the product of the scales is outside [2^-100, 2^100].
 __device__ __forceinline__ float2 output_scale(const float* ga, const float* gw, int b) {
     if (!ga) return make_float2(1.0f, 1.0f);
-    const double p = (double)ga[b] * (double)gw[b];
+    const double p = (double)ld_f32(ga + b) * (double)ld_f32(gw + b);
     if (p < 0x1p-100 && p > 0.0) return make_float2(0x1p-100f, (float)(p * 0x1p100));
     if (p > 0x1p100 && p < 0x1p1000) return make_float2(0x1p100f, (float)(p * 0x1p-100));
     return make_float2((float)p, 1.0f);

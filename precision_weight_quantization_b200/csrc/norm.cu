@@ -226,14 +226,15 @@ __global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxTh
     uint4 v[kVec], wv[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
-        v[i] = i * threads + (int)threadIdx.x < a.vecs ? ld_stream_v4(x + i * step) : make_uint4(0u, 0u, 0u, 0u);
+        v[i] = i * threads + (int)threadIdx.x < a.vecs ? ld_once_v4(x + i * step) : make_uint4(0u, 0u, 0u, 0u);
+    const float amax_in = kMx ? 0.0f : ld_f32(a.amax + b);
     if (a.res.ptr) {
         const char* res = a.res.ptr + (int64_t)b * a.res.bstride + (int64_t)m * a.res.rstride + 16 * threadIdx.x;
         char* h = a.h.ptr + (int64_t)b * a.h.bstride + (int64_t)m * a.h.rstride + 16 * threadIdx.x;
         uint4 u[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            u[i] = i * threads + (int)threadIdx.x < a.vecs ? ld_stream_v4(res + i * step) : make_uint4(0u, 0u, 0u, 0u);
+            u[i] = i * threads + (int)threadIdx.x < a.vecs ? ld_once_v4(res + i * step) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             v[i] = add_bf16(v[i], u[i]);
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxTh
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         const int k = i * threads + (int)threadIdx.x;
-        wv[i] = k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
+        wv[i] = k < a.vecs ? ld_v4(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
         s += squares(v[i]);
     }
     s = warp_sum(s);
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kMaxThreads, (kVec == 5 ? 768 : 1024) / kMaxTh
     float gs = 0.0f, g6 = 0.0f, r6 = 0.0f;
     bool fast6 = false;
     if (!kMx) {
-        gs = __fdiv_rn(__ldg(a.amax + b), 2688.0f);
+        gs = __fdiv_rn(amax_in, 2688.0f);
         g6 = __fmul_rn(6.0f, gs);
         r6 = __frcp_rn(g6);
         fast6 = div_fast_ok(g6);
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     uint4 held[kHoldW ? kVec : 1];
     auto weight = [&](int i) {
         const int k = i * tpr + t;
-        return k < a.vecs ? __ldg(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
+        return k < a.vecs ? ld_v4(a.weight + k) : make_uint4(0u, 0u, 0u, 0u);
     };
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -427,11 +428,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     int flip = 0;
     bool alive = true;
     int waits = a.ring;
-    float rstd_next = first < a.total_rows ? __ldg(a.rstd + first) : 0.0f;
+    float rstd_next = first < a.total_rows ? ld_f32(a.rstd + first) : 0.0f;
     for (uint64_t r64 = first; r64 < a.total_rows; r64 += stride, flip ^= 1) {
         const uint32_t r = (uint32_t)r64;
         const float rstd = rstd_next;   // loaded a row ahead
-        if (r64 + stride < a.total_rows) rstd_next = __ldg(a.rstd + r + stride);
+        if (r64 + stride < a.total_rows) rstd_next = ld_f32(a.rstd + r + stride);
         // once a wait has given up the outputs are unspecified: no further copies, and waits only for those in flight
         if (waits > 0 && !mbar_wait_bounded(full + 8u * st, phase, kNormWaitNs)) {
             atomicOr(&g_norm_error, kErrTmaTimeout);
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* parts, 
         float t[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            t[i] = d < D && p + 32 * i < n_parts ? __ldg(parts + (int64_t)(p + 32 * i) * D + d) : 0.0f;
+            t[i] = d < D && p + 32 * i < n_parts ? ld_f32(parts + (int64_t)(p + 32 * i) * D + d) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v += t[i];
     }

@@ -66,6 +66,28 @@ cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned bloc
 __device__ __forceinline__ void let_later_kernels_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Loads of such kernels.  griddepcontrol.wait makes the earlier kernels' writes
+// visible to ordinary loads; the non-coherent path (ld.global.nc, __ldg) is
+// defined only for memory that nothing writes during the kernel's lifetime,
+// which here begins before those writes (and an in-place output is written by
+// the kernel itself).  _once: not kept in L1.
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_f32(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // Grid size for a persistent elementwise kernel: enough CTAs to cover
 // `work_ctas`, at most `per_sm` resident CTAs per SM.
 int persistent_grid(int64_t work_ctas, int per_sm);

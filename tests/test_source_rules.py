@@ -60,3 +60,26 @@ def test_acquire_spin_loops_read_the_timer():
             body = body[:body.index("}")]
             assert "globaltimer_ns" in body and "break" in body, (name, body[:200])
     assert loops >= 1
+
+
+def test_kernels_launched_early_read_coherently():
+    """A kernel that may start while the one ahead of it still runs
+    (launch_early) reads what that one writes after griddepcontrol.wait.  The
+    non-coherent path (ld.global.nc, __ldg) is defined only for memory that
+    nothing writes while the kernel lives, so such files use neither it nor
+    a helper of the headers that is made of it."""
+    files = {name: strip_comments(text) for name, text in sources().items()}
+    helpers = set()
+    for name, code in files.items():
+        for m in re.finditer(r"__device__ __forceinline__ [\w:]+ (\w+)\([^)]*\) \{(.*?)\n\}", code, flags=re.S):
+            if re.search(r"\.nc\b|__ldg\s*\(", m.group(2)):
+                helpers.add(m.group(1))
+    assert {"ld_stream_v4", "ld_stream_v2", "ld_hint_v4", "ld_nc_v8"} <= helpers, helpers
+    early = [n for n, code in files.items() if n.endswith(".cu") and re.search(r"\blaunch_early\s*\(", code)]
+    assert early
+    for name in early:
+        code = files[name]
+        assert "wait_for_earlier_kernels();" in code, name
+        bad = re.findall(r"__ldg\s*\(|\.nc\b|\b(?:%s)\s*\(" % "|".join(sorted(helpers)), code)
+        assert not bad, (name, bad)
+        assert "__restrict__" not in code, name    # const __restrict__ lets the compiler choose that path
