@@ -674,7 +674,9 @@ def nvfp4_matmul(a: torch.Tensor, a_sb: torch.Tensor, a_global_scale: torch.Tens
     """BF16 y = a w^T of NVFP4 operands (W4A4): packed codes a [.., M, K/2]
     and w [.., N, K/2], E4M3 block scales in the tensor-core tile layout
     (nvfp4_quant_grouped_mma, scales_to_mma, rms_norm_nvfp4), FP32 global
-    scales [B].  As mxfp8_matmul otherwise."""
+    scales [B].  K % 32 == 16 needs padded code rows: rms_norm_nvfp4 makes
+    them, nvfp4_quant_grouped_mma writes them when given through its ``out``.
+    As mxfp8_matmul otherwise."""
     _check_dtype(a, (torch.uint8,), "a")
     _check_dtype(w, (torch.uint8,), "w")
     da, dw = _desc(a, "a", True), _desc(w, "w", True)
@@ -744,14 +746,21 @@ def rms_norm_nvfp4(x: torch.Tensor, weight: torch.Tensor, amax: torch.Tensor,
                    global_scale: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None):
     """rms_norm_mxfp8 with NVFP4 output for a given activation amax (float32
     [B], an NVFP4ActivationObserver's).  Returns (packed codes uint8
-    [.., M, D/2], block scales, global scales float32 [B], h)."""
+    [.., M, D/2], block scales, global scales float32 [B], h); with mma=True
+    the code rows are 16-byte aligned, as nvfp4_matmul reads them (D % 32 == 16
+    gives rows padded by 8 bytes)."""
     px, pr, ph, dx, h = _norm_inputs(x, weight, residual, h)
     B, M, S = dx.batch, dx.rows, dx.cols // 16
     n = _tile_bytes(B, M, S) if mma else B * M * S
     dev = x.device
     if out is None:
-        out = torch.empty(*x.shape[:-1], dx.cols // 2, dtype=torch.uint8, device=dev)
+        cols = dx.cols // 2
+        # the product reads code rows that are 16-byte aligned: an odd number of 16-element blocks pads its rows
+        wide = -(-cols // 16) * 16 if mma else cols
+        out = torch.empty(*x.shape[:-1], wide, dtype=torch.uint8, device=dev)
         do = _new_desc(out, dx, dx.cols)
+        if wide != cols:
+            out = out[..., :cols]
     else:
         _check_dtype(out, (torch.uint8,), "out")
         do = _desc(out, "out", True)

@@ -322,6 +322,32 @@ def test_norm_then_product(P, fmt, M):
     assert bool(((out.double().cpu()[None] - exact).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("shape", [(20, 1040), (1, 48), (2, 5, 16)], ids=lambda s: "x".join(map(str, s)))
+def test_norm_of_odd_sixteens_then_product(P, shape):
+    """D % 32 == 16: the norm's own output goes into the product, the weight's
+    codes into rows padded to 16 bytes through out=."""
+    D, N, B = shape[-1], 100, shape[0] if len(shape) == 3 else 1
+    x, w, r = inputs(shape, 69)
+    lin = W.random_bf16(shape[:-2] + (N, D), seed=70, std=0.02, device=DEV)
+    wide = torch.empty(lin.shape[:-1] + (D // 2 + 8,), dtype=torch.uint8, device=DEV)
+    o, sb, gw = P.nvfp4_quant_grouped_mma([[lin]], out=[[wide[..., :D // 2]]])
+    y, _, _ = reference(x, w, r, 1e-6)
+    am = torch.full((B,), float(amax_of(y)), device=DEV)
+    packed, scale, ga, _ = P.rms_norm_nvfp4(x.to(DEV), w.to(DEV), am, r.to(DEV))
+    assert packed.shape == shape[:-1] + (D // 2,)
+    out = P.nvfp4_matmul(packed, scale, ga, o[0][0], sb[0][0], gw[0])
+
+    def operand(p, s, rows, gs):
+        p = p.cpu().reshape(B, rows, -1)
+        return Operand("nvfp4", torch.stack((p & 15, p >> 4), -1).flatten(-2),
+                       P.scales_from_mma(s, (B, rows, D // 16)).cpu(), gs.cpu())
+
+    exact, bound = exact_and_bound(operand(packed, scale, shape[-2], ga), operand(o[0][0], sb[0][0], N, gw[0]))
+    assert bool(((out.double().cpu().reshape(exact.shape) - exact).abs() <= bound).all())
+    dense = P.rms_norm_nvfp4(x.to(DEV), w.to(DEV), am, r.to(DEV), mma=False)[0]
+    assert dense.is_contiguous() and torch.equal(dense, packed)
+
+
 # ------------------------------------------------------------------ backward
 
 def backward_inputs(shape, seed, dh=True):
