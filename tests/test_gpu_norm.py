@@ -396,6 +396,18 @@ def test_backward_against_the_formula(P, shape, dh):
     assert none is None and torch.equal(only, dx)
 
 
+@pytest.mark.parametrize("dh", (True, False), ids=("dh", "no_dh"))
+@pytest.mark.parametrize("shape", [(650, 4112), (650, 5120), (650, 5136), (650, 7168), (650, 8192), (650, 8208),
+                                   (650, 12288), (650, 16384), (320, 16400), (320, 24592), (310, 32768),
+                                   (2, 325, 4624)], ids=lambda s: "x".join(map(str, s)))
+def test_backward_of_every_launch_shape(P, shape, dh):
+    """Both sides of every width at which the launch changes (4096, 5120, 8192,
+    16384 columns), with more rows than all CTAs take at once: every ring
+    of rows comes around and every CTA adds several rows into its dweight.
+    The bounds of the test above hold: 32 terms of c in a thread at most."""
+    test_backward_against_the_formula(P, shape, dh)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_gradients_against_differences(P, fmt):
     """Autograd through the fake-quantised norm is the gradient of the norm
