@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
             if constexpr (kChunk == 16) tmem_ld16(row + c0, v);
             else tmem_ld32(row + c0, v);
             tmem_ld_wait();
-            if (steps == 0 || !ok) {
+            if (!ok) {
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c) v[c] = 0u;
             }
@@ -370,11 +370,11 @@ struct PairArgs {
     int tile_t, t_band_box;      // tokens per tile, scale bands per tile
     uint32_t stages, stage, scale_stage, out_at, scales_at;   // ring: stages, bytes of codes and of scales per stage
     uint32_t scale_bufs;         // scale buffers in TMEM
-    uint32_t w_tiles, t_tiles, tiles;
+    uint32_t t_tiles, tiles;
     FastDiv per_batch, per_group;   // w_tiles * t_tiles, w_tiles * kGroup
 };
 
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 10;                                     // as many as ever fit (MXFP8, tiles of 32 tokens)
 constexpr uint32_t kPairSmem = 232448u - 512u;   // dynamic shared memory of a CTA (the rest is static)
 
 template <ProductFormat kF>
@@ -820,7 +820,6 @@ cudaError_t launch_pairs(const Product& p, EncodeTiledFn encode, cudaStream_t s)
     a.n = (int)p.w.rows;
     a.m = (int)p.a.rows;
     a.last_mmas = (int)((row_bytes - (int64_t)(a.steps - 1) * kStepBytes + 31) / 32);
-    a.w_tiles = (uint32_t)w_tiles;
     a.t_tiles = (uint32_t)t_tiles;
     a.tiles = (uint32_t)(p.a.batch * w_tiles * t_tiles);
     a.per_batch = make_fastdiv((uint32_t)(w_tiles * t_tiles));
