@@ -94,14 +94,21 @@ PROFILES = {
 
 
 def source_sha256(kernel_file):
-    """sha256 of the code of a kernel file and the shared device header, with
-    comments and blank space left out (a comment edit is no kernel change)."""
+    """sha256 of the code of a kernel file, the shared device header and the
+    further device headers (.cuh) that the file includes, with comments and
+    blank space left out (a comment edit is no kernel change)."""
     import hashlib
     import re
-    h = hashlib.sha256()
-    for f in (kernel_file, "pwq_device.cuh"):
+
+    def read(f):
         with open(os.path.join(ROOT, CSRC, f), encoding="utf-8") as fh:
-            text = fh.read()
+            return fh.read()
+
+    h = hashlib.sha256()
+    shared = "pwq_device.cuh"
+    included = [f for f in re.findall(r'^#include "(\w+\.cuh)"', read(kernel_file), flags=re.M) if f != shared]
+    for f in [kernel_file, shared] + sorted(included):
+        text = read(f)
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
         text = re.sub(r"//[^\n]*", "", text)
         h.update("\n".join(line.strip() for line in text.splitlines() if line.strip()).encode())

@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpwq.so")
 SOURCES = ["pwq_api.cu", "fp8_block.cu", "mxfp8.cu", "nvfp4.cu", "requant.cu", "observer.cu", "selftest.cu",
            "scale_layout.cu", "matmul.cu", "norm.cu"]
-HEADERS = ["pwq_device.cuh", "pwq_internal.h", "pwq_tcgen05.cuh"]
+HEADERS = ["pwq_device.cuh", "pwq_early.cuh", "pwq_internal.h", "pwq_tcgen05.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 EXACT = ["-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false"]

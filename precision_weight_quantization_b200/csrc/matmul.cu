@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cuda.h>
 
+#include "pwq_early.cuh"
 #include "pwq_internal.h"
 #include "pwq_tcgen05.cuh"
 

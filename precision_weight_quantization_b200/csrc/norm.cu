@@ -22,6 +22,7 @@
 // tie test on eight low halves at once.
 #include <algorithm>
 
+#include "pwq_early.cuh"
 #include "pwq_internal.h"
 
 namespace pwq {

@@ -76,6 +76,25 @@ def test_recorded_traffic_fresh_and_stale(tmp_path, monkeypatch):
     assert bench.recorded_traffic("other")[0] is None
 
 
+def test_source_hash_covers_the_included_device_headers(tmp_path, monkeypatch):
+    # a kernel's helpers in a header of their own are part of what a summary was taken on
+    _fake_tree(tmp_path, monkeypatch)
+    csrc = tmp_path / bench.CSRC
+    plain = bench.source_sha256("k.cu")
+    (csrc / "pwq_mma.cuh").write_text("int mma_v1;\n")
+    assert bench.source_sha256("k.cu") == plain
+    (csrc / "k.cu").write_text('#include "pwq_device.cuh"\n#include "pwq_mma.cuh"\nint kernel_v1;\n')
+    sha = bench.source_sha256("k.cu")
+    (csrc / "pwq_mma.cuh").write_text("int mma_v1;   // a comment\n")
+    assert bench.source_sha256("k.cu") == sha
+    (csrc / "pwq_mma.cuh").write_text("int mma_v2;\n")
+    assert bench.source_sha256("k.cu") != sha
+    # the products' tensor-core helpers, and the launch helpers of both
+    code = {f: open(os.path.join(ROOT, bench.CSRC, f)).read() for f in ("matmul.cu", "norm.cu")}
+    assert '#include "pwq_tcgen05.cuh"' in code["matmul.cu"]
+    assert all('#include "pwq_early.cuh"' in c for c in code.values())
+
+
 def test_every_profile_summary_parses():
     # each committed summary names its traffic and the source hash it was taken on
     for op, (md, src) in bench.PROFILES.items():
