@@ -423,7 +423,8 @@ pwq_status nvfp4_quant_grouped_mma(int n_groups, const int* group_sizes, const p
  * write them), FP32 global scales [B] of each operand.  The products of
  * codes and scales are exact and accumulated by the tensor core in FP32 (the
  * order of the sum is the hardware's; calls with the same arguments give
- * the same bits); the FP32 sum times ga_b gw_b is rounded to BF16 once.
+ * the same bits; a partial sum beyond FP32's range is infinite); the FP32 sum
+ * times ga_b gw_b, both products in FP32, is rounded to BF16.
  * NaN scale bytes (0xff UE8M0, 0x7f E4M3) and NaN codes give NaN in the
  * rows and columns that they meet.
  *

@@ -886,7 +886,9 @@ def rms_norm_fake_quant_ste(x: torch.Tensor, weight: torch.Tensor, residual: Opt
                             format: str = "mxfp8", amax: Optional[torch.Tensor] = None, eps: float = 1e-6):
     """rms_norm_fake_quant with its backward pass (the quantiser straight
     through, verl NVFP4 QAT article 2.3).  Returns (y, h); h is x itself
-    without a residual."""
+    without a residual.  No second derivative.  As with any operation of
+    torch, a backward pass is captured into a graph only while no eager graph of
+    the same leaves is alive (torch raises otherwise)."""
     if residual is None:
         return _RMSNormSTE.apply(x, weight, None, format, amax, eps), x
     return _RMSNormSTE.apply(x, weight, residual, format, amax, eps)

@@ -282,6 +282,18 @@ def test_nan_scales_stay_in_their_row_and_column(P, fmt, M):
     assert bool(y.isnan()[bad].all()) and torch.equal(y[~bad], ref[~bad])
 
 
+@pytest.mark.parametrize("M", (3, 40, 300))
+@pytest.mark.parametrize("sa,sw", [(0, 254), (254, 0), (1, 253), (0, 127), (0, 0), (64, 63), (60, 60), (70, 50), (190, 170)])
+def test_block_scales_over_their_range(P, M, sa, sw):
+    """UE8M0 scales from 2^-127 to 2^127: integers times 2^(sa + sw - 254), exact
+    in FP32, results in BF16's subnormal range and below it among them."""
+    a, w = integer_operand("mxfp8", 1, M, 128, 56), integer_operand("mxfp8", 1, 130, 128, 57)
+    a.scales[:], w.scales[:] = sa, sw
+    want = bmm64(E4M3[a.codes.long()], E4M3[w.codes.long()]) * 2.0 ** (sa + sw - 254)
+    y = call(P, *(Operand("mxfp8", o.codes, o.scales) for o in (a, w)))
+    assert torch.equal(y.cpu(), want.float().bfloat16())
+
+
 def test_global_scales_over_their_range(P):
     """Scales whose product leaves the FP32 range although the result does not
     (and results that overflow or underflow)."""

@@ -514,6 +514,67 @@ def test_streams_repeats_and_graph(P):
     assert eager[0].requires_grad
 
 
+def test_training_step_captured_through_autograd(P):
+    """Forward and backward of the autograd form in one graph, replayed with
+    rewritten inputs: the bits of an eager step."""
+    x, w, r = (t.to(DEV) for t in inputs((200, 1056), 99))
+    dy, dh = (W.random_bf16((200, 1056), seed=s, std=0.5, device=DEV) for s in (100, 101))
+
+    def step(*leaves):
+        lv = [t.detach().requires_grad_() for t in leaves]     # no eager graph of these leaves is alive
+        y, h = P.rms_norm_fake_quant_ste(lv[0], lv[1], lv[2])
+        return (y.detach(), h.detach()) + torch.autograd.grad((y, h), lv, (dy, dh))
+
+    sx, sw, sr = x.clone(), w.clone(), r.clone()
+    step(sx, sw, sr)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(sx, sw, sr)
+    for a, b in ((x, r), (x.flip(0).contiguous(), r.roll(3, 0))):
+        sx.copy_(a)
+        sr.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, step(a, w, b)))
+
+
+def test_two_streams_captured_in_one_graph(P):
+    """A capture that forks: the weight is quantised on a second stream beside
+    the norms, the product joins both; kernels with programmatic and full
+    dependencies in one graph."""
+    D = 1024
+    x, w, r = (t.to(DEV) for t in inputs((40, D), 102))
+    lin = W.random_bf16((520, D), seed=103, std=0.05, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step(fork):
+        cur = torch.cuda.current_stream()
+        c, s, h = P.rms_norm_mxfp8(x, w, r)
+        if fork:
+            side.wait_stream(cur)
+        with torch.cuda.stream(side if fork else cur):
+            (q,), (sq,) = P.mxfp8_quant_grouped_mma([lin])
+        c2, s2, h2 = P.rms_norm_mxfp8(h, w, x)
+        if fork:
+            cur.wait_stream(side)
+        y = P.mxfp8_matmul(c2, s2, q, sq)
+        y2 = torch.empty_like(y)
+        y2.zero_()
+        P.mxfp8_matmul(c, s, q, sq, out=y2)
+        return y, y2, h2
+
+    ref = step(False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(True)
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
 def test_refusals(P):
     x, w, r = (t.to(DEV) for t in inputs((4, 64), 95))
     one = torch.ones(1, device=DEV)
