@@ -85,7 +85,8 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 //
 // Bound by the weight's bytes and, for small weights, by the launch and the
 // first loads' latency: 19456 x 2560 at one token takes 7.0 us in NVFP4
-// (28 MB, 4.0 TB/s), 2560 x 9728 at eight in MXFP8 7.2 us (26 MB, 3.6 TB/s).
+// (28 MB, 4.0 TB/s), 2560 x 9728 at eight in MXFP8 7.2 to 7.9 us on several
+// GPUs (26 MB, 3.3 to 3.6 TB/s).
 //
 // Warps 0..3 epilogue, 4 and 6 TMA producers (codes, scales), 5 MMA issuer and TMEM owner.
 
@@ -314,16 +315,18 @@ __global__ void __launch_bounds__(kTokThreads, 2) tokens_kernel(const __grid_con
 // persistent, one pair per two SMs, tiles in groups of kGroup token tiles so
 // that the pairs at work share operands in L2.
 //
-// What bounds it.  Power: under these products the SMs run at 1.4 to 1.65 GHz,
-// and what saves clocks without saving energy saves no time.  8192^3 runs at
-// 2.84 PFLOP/s (MXFP8, 1.7 times the measured BF16 rate) and 5.5 (NVFP4, 3.4
-// times).  In clocks: a step of MXFP8 takes 512, its MMAs; one of NVFP4 takes
-// 643, what issuing twelve scale copies beside four MMAs takes, and about 800
-// while the epilogue warp of the same scheduler is at work; a tile's start
-// costs 660 and 1040 (its accumulator shares columns with the one before).
-// Issuing the copies from a warp of their own brought the NVFP4 step to 490 to
-// 610 clocks, and the products 1 to 3 % more time.  The loads bound nothing:
-// without them a step takes the same.
+// What bounds it.  In steady use, power: every sample under these products
+// shows the 1000 W cap, with the SMs at 1.2 to 1.43 GHz (MXFP8 8192^3 1.21 GHz,
+// NVFP4 4096 x 19456 x 2560 1.43), and what saves clocks without saving energy
+// saves no time there.  8192^3 runs at 2.6 PFLOP/s sustained and 3.07 in six
+// launches after a pause (MXFP8), 4.9 and 5.8 (NVFP4).  In clocks: a step of
+// MXFP8 takes 512, its MMAs; one of NVFP4 takes 643 at 256 tokens, what issuing
+// twelve scale copies beside four MMAs takes, and about 800 while the epilogue
+// warp of the same scheduler is at work; a tile's start costs 660 and 1040 (its
+// accumulator shares columns with the one before).  Issuing the copies from a
+// warp of their own brought the NVFP4 step to 490 to 610 clocks: one launch
+// alone 85 -> 76 us, eight in a row 84.3 -> 81.9, forty in a row 89.0 -> 92.6.
+// The loads bound nothing: without them a step takes the same.
 //
 // Issue: the issuer tests the next step's barriers while it issues a step and
 // waits only when the test failed (two waits at the start of each step made
@@ -756,10 +759,12 @@ cudaError_t launch_tokens(const Product& p, EncodeTiledFn encode, cudaStream_t s
 }
 
 // Tokens per tile of the pair kernel: the fewest (waves of tiles) x (time of
-// a tile).  A step was measured at 0.39 / 0.35 / 0.30 us for 256 / 192 / 128
-// tokens, close to the bytes that it brings in (256 weight rows, the tile's
-// tokens, scales worth 24 rows); a tile's start and the part of its epilogue
-// that nothing hides cost about two steps.
+// a tile).  A step takes about as long as the bytes that it brings in (256
+// weight rows, the tile's tokens, scales worth 24 rows): measured, for 256 /
+// 192 / 128 / 64 tokens, 0.44 / 0.34 / 0.29 / 0.26 us in NVFP4 and 0.51 / 0.31 /
+// 0.27 / 0.24 in MXFP8 (9472 tokens, 4096 weight rows; at 256 the power cap
+// slows MXFP8).  A tile's start and the part of its epilogue that nothing hides
+// take 1.1 us in NVFP4, 0.3 to 0.8 in MXFP8: about two steps.
 int pair_tile_tokens(int64_t m, int64_t w_tiles, int64_t batch, int64_t pairs, int64_t steps) {
     int best = 256;
     int64_t best_cost = -1;
